@@ -420,6 +420,158 @@ int cpattn_fwd_noalloc(const void* q, const void* k, const void* v,
                        int32_t* status, void* stream);
 
 /*
+ * RMS norm of every query and key head with the rotary position embedding in
+ * the same pass, and its gradients.  The source pages have no counterpart to
+ * these calls: they make the Q and K that cpattn_fwd takes (and the gradients that
+ * cpattn_bwd gives go back through them).
+ *
+ * For a head row x [D] of a token at position p, with weight w [D]:
+ *   n = x / sqrt(mean(x^2) + eps) * w            (n = x without weights)
+ *   y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin
+ * for the R / 2 pairs (a, b) of the first R = rotary_dim features, pair j with
+ * angle j of position p; the features from R on are n.  Pairs are (j, j + R/2)
+ * (interleaved = 0) or (2j, 2j + 1) (interleaved = 1).
+ *
+ *   q, k          bf16 [T, H, D] and [T, num_kv_heads, D], 16-byte aligned; a
+ *                 token's heads are contiguous and q_stride / k_stride are the
+ *                 elements from token to token (>= heads * D, a multiple of 8),
+ *                 so slices of one projection's output can be passed as they
+ *                 are.  q_out, k_out likewise; an output may be its own input
+ *                 (in place), other overlaps are not allowed.
+ *   positions     device int32 [T]; any order.  May be NULL without a table.
+ *   rope_table    device float [max_position, R], 16-byte aligned: the cosines
+ *                 of a position's R / 2 angles, then their sines.  R a multiple
+ *                 of 16, 16 .. D.  NULL: no rotation.
+ *   q_weight, k_weight  bf16 [D], 16-byte aligned, shared by the heads; both or
+ *                 neither (NULL: no norm).  Table and weights must not both be
+ *                 missing.  eps > 0 (ignored without weights).
+ *   status        device int32 [1] or NULL: set to CPATTN_ERR_INVALID_ARG when a
+ *                 position is outside [0, max_position), else left as it is.
+ *                 The rows of such a token are left as they were.
+ *   T * (H + num_kv_heads) < 2^31; head_dim D 64 or 128.
+ * Precision: fp32 between the load and the one rounding to bf16.
+ *
+ * cpattn_qk_norm_rope_bwd -- with g the gradient dy rotated back and
+ * hat = x / sqrt(mean(x^2) + eps):
+ *   dw = sum over tokens and heads of g hat,  u = g w,
+ *   dx = (u - hat mean(u hat)) / sqrt(mean(x^2) + eps)   (dx = g without weights)
+ *   dq_out, dk_out  bf16 gradients of the outputs; q, k the call's inputs (not
+ *                 read, and may be NULL, without weights); dq, dk bf16 outputs.
+ *                 dq may be dq_out, and dk dk_out (in place).
+ *   dq_weight, dk_weight  float [D], written whole (NULL without weights).
+ *   workspace     >= cpattn_qk_norm_rope_bwd_workspace_size(D) bytes, 256-byte
+ *                 aligned (NULL without weights).  Sums are taken in a fixed
+ *                 order: equal inputs give equal bits.
+ * A token whose position is outside the table adds nothing to the weights'
+ * gradients.  Both calls enqueue on `stream`; argument errors return before any
+ * launch.
+ */
+int cpattn_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const int32_t* positions,
+                        const float* rope_table, int32_t rotary_dim,
+                        int32_t max_position, const void* q_weight,
+                        const void* k_weight, float eps, int32_t interleaved,
+                        int64_t total_tokens, int32_t num_heads,
+                        int32_t num_kv_heads, int32_t head_dim, void* q_out,
+                        int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                        int32_t* status, void* stream);
+size_t cpattn_qk_norm_rope_bwd_workspace_size(int32_t head_dim);
+int cpattn_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride,
+                            const void* dk_out, int64_t dk_out_stride,
+                            const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const int32_t* positions,
+                            const float* rope_table, int32_t rotary_dim,
+                            int32_t max_position, const void* q_weight,
+                            const void* k_weight, float eps, int32_t interleaved,
+                            int64_t total_tokens, int32_t num_heads,
+                            int32_t num_kv_heads, int32_t head_dim, void* dq,
+                            int64_t dq_stride, void* dk, int64_t dk_stride,
+                            float* dq_weight, float* dk_weight, void* workspace,
+                            size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Paged KV cache.  Keys and values live in pages of page_size tokens (16, 32,
+ * 64, 128 or 256): k_cache and v_cache are bf16 [num_pages, page_size,
+ * num_kv_heads, D], 16-byte aligned, a page contiguous (a run of the packed
+ * layout) and page_stride elements from page to page (>= page_size *
+ * num_kv_heads * D, a multiple of 8; the same for both).  page_table is device
+ * int32 [num_seqs, max_pages]: token p of sequence b is row p % page_size of
+ * page page_table[b, p / page_size].  Entries behind a sequence's last page are
+ * not read.  kv_lens is device int32 [num_seqs]: each sequence's tokens in the
+ * cache, the new ones among them; cu_seqlens [num_seqs + 1] packs the new
+ * tokens, so new token i of the q_len of sequence b stands at position
+ * kv_lens[b] - q_len + i.  cu_seqlens[num_seqs] may be below the token count of
+ * the arrays: the rows behind the last sequence are neither read nor written.
+ * The source pages have no counterpart to these two calls.
+ *
+ * cpattn_paged_append -- writes the new tokens' keys and values into the cache,
+ * the keys with cpattn_qk_norm_rope's norm and rotation on the way, and
+ * optionally the new queries, normed and rotated, to q_out.
+ *   k, v, q, q_out   as cpattn_qk_norm_rope's arrays; v is copied as it is.
+ *                 q may be NULL (then num_heads = 0, q_weight and q_out NULL).
+ *   rope_table, rotary_dim, max_position, interleaved, eps  as there; NULL: no
+ *                 rotation.  k_weight (with q: both or neither) NULL: no norm.
+ *   status        device int32 [1] or NULL: set to CPATTN_ERR_INVALID_ARG (else
+ *                 left as it is) when a token's sequence is not consistent
+ *                 (kv_lens above max_pages * page_size or below its new tokens),
+ *                 its page number is outside [0, num_pages) or its position is
+ *                 outside the table; such a token is left out.
+ *   Two tokens with one place in the cache leave one of them there.
+ *
+ * cpattn_paged_attn -- attention of the new tokens over the cache, their own
+ * keys and values in it:
+ *   O_i = softmax(softmax_scale * q_i K^T) V over the keys 0 .. its position
+ *   (causal = 1) or all kv_lens[b] keys (causal = 0); query head h reads KV head
+ *   h / (H / num_kv_heads).  One new token a sequence is the decoding step;
+ *   many are a prompt chunk.  A row that sees no key has O = 0, LSE = -inf.
+ *   q             bf16 [total_q, H, D], contiguous, 16-byte aligned; H a
+ *                 multiple of num_kv_heads, at most 128 times it.
+ *   max_seqlen, max_kv_len   bounds on every sequence's new tokens and
+ *                 kv_lens; they choose the kernel and size its grid.
+ *   out           bf16 [total_q, H, D] (not q);  lse float [total_q, H] or NULL.
+ *   workspace     >= cpattn_paged_attn_workspace_size(...) bytes, 256-byte
+ *                 aligned; its first bytes hold the error word.  Calls that
+ *                 may overlap need workspaces of their own.
+ * The kernels check cu_seqlens, kv_lens (0 .. max_kv_len and max_pages *
+ * page_size) and the bounds; a violation sets CPATTN_ERR_INVALID_ARG in the
+ * error word (cpattn_poll_error) and writes no output.  A page number outside
+ * [0, num_pages) sets it too; that page's keys and values then count as zeros.
+ * Cache rows from kv_lens on may hold anything, NaN included.  A key that a
+ * row does not see because of causality has to be finite, as its weight 0
+ * multiplies its value.
+ * Precision: fp32 scores, softmax and sums; P is rounded to bf16 for its
+ * product with V; one rounding of O to bf16.  Sums are taken in a fixed order.
+ * Both calls enqueue on `stream`, read all lengths on the device (a captured
+ * call can be replayed with other lengths within its bounds), and return
+ * argument errors before any launch.
+ */
+int cpattn_paged_append(const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, void* k_cache, void* v_cache,
+                        int64_t num_pages, int32_t page_size, int64_t page_stride,
+                        const int32_t* page_table, int32_t max_pages,
+                        const int32_t* cu_seqlens, const int32_t* kv_lens,
+                        int32_t num_seqs, int64_t total_tokens,
+                        int32_t num_kv_heads, int32_t head_dim,
+                        const float* rope_table, int32_t rotary_dim,
+                        int32_t max_position, int32_t interleaved,
+                        const void* q_weight, const void* k_weight, float eps,
+                        const void* q, int64_t q_stride, int32_t num_heads,
+                        void* q_out, int64_t q_out_stride, int32_t* status,
+                        void* stream);
+size_t cpattn_paged_attn_workspace_size(int64_t total_q, int32_t num_seqs,
+                                        int32_t num_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t max_seqlen);
+int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
+                      int64_t num_pages, int32_t page_size, int64_t page_stride,
+                      const int32_t* page_table, int32_t max_pages,
+                      const int32_t* cu_seqlens, const int32_t* kv_lens,
+                      int32_t num_seqs, int64_t total_q, int32_t max_seqlen,
+                      int32_t max_kv_len, int32_t num_heads, int32_t num_kv_heads,
+                      int32_t head_dim, float softmax_scale, int32_t causal,
+                      void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
  * cpattn_poll_error -- synchronise `stream` and return the workspace's error
  * word (CPATTN_OK when every kernel since the last cpattn_fwd on this
  * workspace finished normally), or CPATTN_ERR_CUDA if the stream reports a

@@ -83,6 +83,27 @@ _lib.cpattn_ulysses_layout.argtypes = [_vp, _vp, _i64, _i32, _i64, _i32, _i32, _
 _lib.cpattn_ulysses_layout.restype = ctypes.c_int
 _lib.cpattn_ulysses_seqlens.argtypes = [_vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp]
 _lib.cpattn_ulysses_seqlens.restype = ctypes.c_int
+_f32 = ctypes.c_float
+_lib.cpattn_qk_norm_rope.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _f32,
+                                     _i32, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp]
+_lib.cpattn_qk_norm_rope.restype = ctypes.c_int
+_lib.cpattn_qk_norm_rope_bwd_workspace_size.argtypes = [_i32]
+_lib.cpattn_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+_lib.cpattn_qk_norm_rope_bwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                         _i32, _i32, _vp, _vp, _f32, _i32, _i64, _i32, _i32, _i32,
+                                         _vp, _i64, _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t,
+                                         _vp, _vp]
+_lib.cpattn_qk_norm_rope_bwd.restype = ctypes.c_int
+_lib.cpattn_paged_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _i32,
+                                     _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i32, _i32,
+                                     _vp, _vp, _f32, _vp, _i64, _i32, _vp, _i64, _vp, _vp]
+_lib.cpattn_paged_append.restype = ctypes.c_int
+_lib.cpattn_paged_attn_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32]
+_lib.cpattn_paged_attn_workspace_size.restype = ctypes.c_size_t
+_lib.cpattn_paged_attn.argtypes = [_vp, _vp, _vp, _i64, _i32, _i64, _vp, _i32, _vp, _vp, _i32,
+                                   _i64, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp,
+                                   ctypes.c_size_t, _vp]
+_lib.cpattn_paged_attn.restype = ctypes.c_int
 _lib.cpattn_poll_error.argtypes = [_vp, _vp]
 _lib.cpattn_poll_error.restype = ctypes.c_int
 _lib.cpattn_status_string.argtypes = [ctypes.c_int]
@@ -706,6 +727,322 @@ def merge(o_steps, m_steps, l_steps, *, out_o=None, out_m=None, out_l=None, stre
                            _ptr(out_o), _ptr(out_m), _ptr(out_l), _stream(stream))
     _check(st, "cpattn_merge")
     return out_o, out_m, out_l
+
+
+# ------------------------------------------------- norm + rotation, paged cache --
+
+def _run_on(dev, stream, made, fn, name, *args):
+    """Call ``fn(*args, stream)`` on the tensors' device and on ``stream`` (the
+    device's current stream when None).  ``made`` are the tensors this call
+    allocated: on a stream that is not current, the allocator has to be told
+    who uses them."""
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream.device != dev:
+        raise ValueError("stream must be on %s, got %s" % (dev, stream.device))
+    elif stream != current:
+        for t in made:
+            t.record_stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != OK:
+        raise CpattnError(st, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need_rows(t, name, dev=None, shape=None):
+    """A bf16 CUDA ``[T, heads, D]`` tensor whose tokens' heads are contiguous;
+    returns the elements from token to token."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must be [T, heads, D]" % name)
+    if not t.is_cuda or (dev is not None and t.device != dev):
+        raise ValueError("%s must be on %s, got %s" % (name, dev or "a CUDA device", t.device))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    n, heads, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return heads * d if n <= 1 else st
+
+
+def _need_weights(q_weight, k_weight, D, dev):
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.bfloat16, dev, (D,))
+
+
+def _need_rope(rope_table, dev):
+    """(rotary dim, positions in the table); (0, 0) without a table."""
+    if rope_table is None:
+        return 0, 0
+    _need(rope_table, "rope_table", torch.float32, dev)
+    if rope_table.dim() != 2:
+        raise ValueError("rope_table must be [max_position, rotary_dim]")
+    return rope_table.shape[1], rope_table.shape[0]
+
+
+@_traced("cpattn_qk_norm_rope")
+def qk_norm_rope(q, k, positions, rope_table, *, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, status=None, stream=None):
+    """RMS norm of every query and key head and the rotary position embedding in
+    one pass (``cpattn_qk_norm_rope``); returns ``(q_out, k_out)``.
+
+    ``q [T, H, D]``, ``k [T, Hk, D]``: bf16, slices of one projection's output
+    allowed (a token's heads contiguous).  ``positions``: int32 ``[T]``;
+    ``rope_table``: float32 ``[max_position, R]``, a row the cosines of the
+    position's ``R / 2`` angles, then their sines (both None: no rotation).
+    ``q_weight``, ``k_weight``: bf16 ``[D]`` (both None: no norm).  ``q_out``
+    may be ``q`` and ``k_out`` may be ``k``.  ``status``: int32 ``[1]``, set
+    when a position is outside the table (its rows are left as they were).
+    """
+    qs = _need_rows(q, "q")
+    T, H, D = q.shape
+    dev = q.device
+    if k.dim() != 3:
+        raise ValueError("k must be [T, heads, D]")
+    ks = _need_rows(k, "k", dev, (T, k.shape[1], D))
+    Hk = k.shape[1]
+    rot, max_pos = _need_rope(rope_table, dev)
+    if rope_table is not None:
+        _need(positions, "positions", torch.int32, dev, (T,))
+    _need_weights(q_weight, k_weight, D, dev)
+    made = []
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        made.append(q_out)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+        made.append(k_out)
+    qos = _need_rows(q_out, "q_out", dev, q.shape)
+    kos = _need_rows(k_out, "k_out", dev, k.shape)
+    if status is not None:
+        _need(status, "status", torch.int32, dev, (1,))
+    _run_on(dev, stream, made, _lib.cpattn_qk_norm_rope, "cpattn_qk_norm_rope", _addr(q), qs,
+            _addr(k), ks, _addr(positions) if rope_table is not None else None, _addr(rope_table),
+            rot, max_pos, _addr(q_weight), _addr(k_weight), eps, 1 if interleaved else 0, T, H, Hk,
+            D, _addr(q_out), qos, _addr(k_out), kos, _addr(status))
+    return q_out, k_out
+
+
+@_traced("cpattn_qk_norm_rope_bwd")
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, rope_table, *, q_weight=None, k_weight=None,
+                     eps=1e-6, interleaved=False, dq=None, dk=None, dq_weight=None,
+                     dk_weight=None, workspace=None, status=None, stream=None):
+    """Gradients of :func:`qk_norm_rope` (``cpattn_qk_norm_rope_bwd``); returns
+    ``(dq, dk, dq_weight, dk_weight)``, the weights' in float32 ``[D]`` (None
+    without weights; ``q`` and ``k`` may then be None too).
+
+    ``dq_out``, ``dk_out``: the gradients of its outputs (token strides as the
+    inputs'); the other arguments as in the call being differentiated.
+    """
+    gqs = _need_rows(dq_out, "dq_out")
+    T, H, D = dq_out.shape
+    dev = dq_out.device
+    if dk_out.dim() != 3:
+        raise ValueError("dk_out must be [T, heads, D]")
+    gks = _need_rows(dk_out, "dk_out", dev, (T, dk_out.shape[1], D))
+    Hk = dk_out.shape[1]
+    rot, max_pos = _need_rope(rope_table, dev)
+    if rope_table is not None:
+        _need(positions, "positions", torch.int32, dev, (T,))
+    _need_weights(q_weight, k_weight, D, dev)
+    normed = q_weight is not None or k_weight is not None
+    qs = ks = 0
+    if normed:
+        qs = _need_rows(q, "q", dev, dq_out.shape)
+        ks = _need_rows(k, "k", dev, dk_out.shape)
+    made = []
+
+    def new(shape, dtype):
+        made.append(torch.empty(shape, dtype=dtype, device=dev))
+        return made[-1]
+
+    if dq is None:
+        dq = new((T, H, D), torch.bfloat16)
+    if dk is None:
+        dk = new((T, Hk, D), torch.bfloat16)
+    dqs = _need_rows(dq, "dq", dev, dq_out.shape)
+    dks = _need_rows(dk, "dk", dev, dk_out.shape)
+    if normed:
+        if dq_weight is None:
+            dq_weight = new((D,), torch.float32)
+        if dk_weight is None:
+            dk_weight = new((D,), torch.float32)
+        _need(dq_weight, "dq_weight", torch.float32, dev, (D,))
+        _need(dk_weight, "dk_weight", torch.float32, dev, (D,))
+        if workspace is None:
+            workspace = new(_lib.cpattn_qk_norm_rope_bwd_workspace_size(D), torch.uint8)
+        else:
+            _need(workspace, "workspace", torch.uint8, dev)
+    elif dq_weight is not None or dk_weight is not None:
+        raise ValueError("dq_weight and dk_weight need q_weight and k_weight")
+    if status is not None:
+        _need(status, "status", torch.int32, dev, (1,))
+    _run_on(dev, stream, made, _lib.cpattn_qk_norm_rope_bwd, "cpattn_qk_norm_rope_bwd",
+            _addr(dq_out), gqs, _addr(dk_out), gks, _addr(q) if normed else None, qs,
+            _addr(k) if normed else None, ks,
+            _addr(positions) if rope_table is not None else None, _addr(rope_table), rot, max_pos,
+            _addr(q_weight), _addr(k_weight), eps, 1 if interleaved else 0, T, H, Hk, D, _addr(dq),
+            dqs, _addr(dk), dks, _addr(dq_weight), _addr(dk_weight),
+            _addr(workspace) if normed else None, workspace.numel() if normed else 0,
+            _addr(status))
+    return dq, dk, dq_weight, dk_weight
+
+
+def _need_cache(k_cache, v_cache, page_table, cu_seqlens, kv_lens, dev):
+    """Checks a paged cache; returns the elements from page to page."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.dtype != torch.bfloat16:
+            raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+        if t.device != dev:
+            raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+        if t.dim() != 4:
+            raise ValueError("%s must be [num_pages, page_size, heads, D]" % name)
+        want = 1
+        for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+            if s != want and n > 1:
+                raise ValueError("%s: a page must be contiguous" % name)
+            want *= n
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    pages, size, heads, D = k_cache.shape
+    stride = size * heads * D if pages <= 1 else k_cache.stride(0)
+    if pages > 1 and v_cache.stride(0) != stride:
+        raise ValueError("k_cache and v_cache must have the same page stride")
+    _need(kv_lens, "kv_lens", torch.int32, dev)
+    if kv_lens.dim() != 1:
+        raise ValueError("kv_lens must be [num_seqs]")
+    B = kv_lens.shape[0]
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    _need(page_table, "page_table", torch.int32, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [num_seqs, max_pages]")
+    return stride
+
+
+@_traced("cpattn_paged_append")
+def paged_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, rope_table=None,
+                 interleaved=False, k_weight=None, eps=1e-6, q=None, q_weight=None, q_out=None,
+                 status=None, stream=None):
+    """New keys and values into a paged cache (``cpattn_paged_append``), the keys
+    (and ``q``, to ``q_out``) with the norm and rotation of
+    :func:`qk_norm_rope` on the way; returns ``q_out`` (None without ``q``).
+
+    ``k, v [T, Hk, D]``, ``q [T, H, D]``: bf16, the new tokens packed by
+    ``cu_seqlens [B + 1]``; ``kv_lens [B]``: each sequence's tokens in the
+    cache, the new ones among them (the last ``cu[b + 1] - cu[b]``); caches bf16
+    ``[num_pages, page_size, Hk, D]``; ``page_table [B, max_pages]``: int32.
+    ``status``: int32 ``[1]``, set when a token could not be placed.
+    """
+    ks = _need_rows(k, "k")
+    T, Hk, D = k.shape
+    dev = k.device
+    vs = _need_rows(v, "v", dev, k.shape)
+    page_stride = _need_cache(k_cache, v_cache, page_table, cu_seqlens, kv_lens, dev)
+    if k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("k and k_cache must share heads and D")
+    rot, max_pos = _need_rope(rope_table, dev)
+    _need_weights(q_weight, k_weight, D, dev)
+    made = []
+    H = qs = qos = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, heads, D]")
+        H = q.shape[1]
+        qs = _need_rows(q, "q", dev, (T, H, D))
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+            made.append(q_out)
+        qos = _need_rows(q_out, "q_out", dev, q.shape)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    if status is not None:
+        _need(status, "status", torch.int32, dev, (1,))
+    _run_on(dev, stream, made, _lib.cpattn_paged_append, "cpattn_paged_append", _addr(k), ks,
+            _addr(v), vs, _addr(k_cache), _addr(v_cache), k_cache.shape[0], k_cache.shape[1],
+            page_stride, _addr(page_table), page_table.shape[1], _addr(cu_seqlens),
+            _addr(kv_lens), kv_lens.shape[0], T, Hk, D, _addr(rope_table), rot, max_pos,
+            1 if interleaved else 0, _addr(q_weight), _addr(k_weight), eps, _addr(q), qs, H,
+            _addr(q_out), qos, _addr(status))
+    return q_out
+
+
+def paged_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen):
+    n = _lib.cpattn_paged_attn_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim,
+                                              max_seqlen)
+    if n == 0:
+        raise CpattnError(ERR_INVALID_ARG, "cpattn_paged_attn_workspace_size")
+    return n
+
+
+def alloc_paged_workspace(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
+                          device=None):
+    """A device workspace sized for :func:`paged_attn` (torch-owned)."""
+    n = paged_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+@_traced("cpattn_paged_attn")
+def paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, max_seqlen, max_kv_len,
+               softmax_scale=None, causal=True, out=None, lse=None, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache that holds their keys and
+    values already (``cpattn_paged_attn``); returns ``(out, lse)``.
+
+    ``q [T, H, D]``: bf16, contiguous, packed by ``cu_seqlens [B + 1]``;
+    ``k_cache, v_cache [num_pages, page_size, Hk, D]``: bf16, ``H`` a multiple
+    of ``Hk``; ``page_table [B, max_pages]``, ``kv_lens [B]``: int32 (see
+    :func:`paged_append`).  ``max_seqlen`` and ``max_kv_len`` bound every
+    sequence's new tokens and cache length.  Rows behind ``cu_seqlens[B]`` are
+    not written.
+    """
+    qs = _need_rows(q, "q")
+    T, H, D = q.shape
+    dev = q.device
+    if qs != H * D:
+        raise ValueError("q must be contiguous")
+    page_stride = _need_cache(k_cache, v_cache, page_table, cu_seqlens, kv_lens, dev)
+    pages, size, Hk, _ = k_cache.shape
+    if k_cache.shape[3] != D:
+        raise ValueError("q and k_cache must share D")
+    B = kv_lens.shape[0]
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    made = []
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        made.append(out)
+    else:
+        _need(out, "out", torch.bfloat16, dev, q.shape)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        made.append(lse)
+    else:
+        _need(lse, "lse", torch.float32, dev, (T, H))
+    if workspace is None:
+        workspace = alloc_paged_workspace(T, B, H, Hk, D, max_seqlen, dev)
+        made.append(workspace)
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+    _run_on(dev, stream, made, _lib.cpattn_paged_attn, "cpattn_paged_attn", _addr(q),
+            _addr(k_cache), _addr(v_cache), pages, size, page_stride, _addr(page_table),
+            page_table.shape[1], _addr(cu_seqlens), _addr(kv_lens), B, T, max_seqlen, max_kv_len,
+            H, Hk, D, softmax_scale, 1 if causal else 0, _addr(out), _addr(lse), _addr(workspace),
+            workspace.numel())
+    return out, lse
 
 
 def poll_error(workspace, stream=None):

@@ -20,15 +20,11 @@ constexpr size_t kAlign = 256;
 
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-struct DeviceInfo {
-  int num_sms = 0;
-  int cc_major = 0;
-  int cc_minor = 0;
-};
-
 std::mutex g_mu;
 std::unordered_map<int, DeviceInfo> g_devices;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
 
 int device_info(DeviceInfo* out) {
   int dev = 0;
@@ -55,6 +51,8 @@ int device_info(DeviceInfo* out) {
   }
   return CPATTN_OK;
 }
+
+namespace {
 
 // Tensor map over a packed bf16 [T, H, D] tensor: dims (D, H, T), box
 // (64, 1, 128) with 128-byte swizzle -- one 128-token x 64-feature slab of one

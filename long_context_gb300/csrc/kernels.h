@@ -131,6 +131,15 @@ struct FwdArgs {
 
 bool aligned(const void* p, size_t a);
 
+struct DeviceInfo {
+  int num_sms = 0;
+  int cc_major = 0;
+  int cc_minor = 0;
+};
+
+// Properties of the current device (cached); a cpattn_status.
+int device_info(DeviceInfo* out);
+
 // Host-checkable argument rules of the forward calls; a cpattn_status.
 int check_fwd(const FwdArgs& a);
 
@@ -187,5 +196,110 @@ cudaError_t launch_bwd_dq(const CUtensorMap& tq, const CUtensorMap& tk,
 
 cudaError_t launch_merge(const MergeParams& p, int D, bool bf16_out,
                          int num_sms, cudaStream_t stream);
+
+// Norm + rotation (norm_rope.cu).  Inputs and outputs are token-major rows of
+// whole heads, [T, heads, D] with a token stride in elements; `table` (null: no
+// rotation) is float [max_pos, rot]; both weights are null or neither.  With a
+// page table the kernel also copies v, takes positions from cu_seqlens and
+// kv_lens, and k_out / v_out are the paged caches (q_heads 0: no queries).
+struct NormRopeParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_out, *k_out, *v_out;
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  const __nv_bfloat16 *q_weight, *k_weight;
+  const int* positions;
+  const float* table;
+  int rot, max_pos, q_heads, kv_heads;
+  long long total_tokens;
+  float eps;
+  int* status;
+  const int *cu_seqlens, *kv_lens, *page_table;
+  int num_seqs, num_pages, page_shift, max_pages;
+  long long page_stride;
+};
+
+cudaError_t launch_norm_rope(const NormRopeParams& p, int D, bool interleaved,
+                             cudaStream_t stream);
+
+constexpr int kNormRopeBwdCtas = 1024;  // at most this many rows of partial weight gradients
+
+struct NormRopeBwdParams {
+  const __nv_bfloat16 *dq_out, *dk_out, *q, *k;
+  __nv_bfloat16 *dq, *dk;
+  long long dq_out_stride, dk_out_stride, q_stride, k_stride, dq_stride, dk_stride;
+  const __nv_bfloat16 *q_weight, *k_weight;
+  const int* positions;
+  const float* table;
+  int rot, max_pos, q_heads, kv_heads;
+  long long total_tokens;
+  float eps;
+  int* status;
+  float* partial;  // [CTAs, D]
+  int q_ctas;      // CTAs that take the query heads (set by the launch)
+};
+
+cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, float* dqw,
+                                 float* dkw, int num_sms, cudaStream_t stream);
+
+// Attention over a paged KV cache (paged_*.cu).  A row is one (token, query
+// head of the KV head's group) pair; the rows of a sequence for one KV head are
+// numbered token * group + head and cut into blocks of `rows` aligned to their
+// end (block 0 may be short).  An item is one block; an item's visible keys
+// are cut into splits of whole units (of `unit` keys), and the attention
+// kernels run one CTA per (split, KV head).
+constexpr int kPagedMaxGroup = 128;
+
+// One split, written by the schedule kernel (two 16-byte loads).
+struct alignas(16) PagedWork {
+  int tok0, q_len, kv_len, seq;
+  int blk;           // row block
+  int kv_lo, kv_hi;  // keys [kv_lo, kv_hi), kv_lo a multiple of the unit
+  int slot;          // slot of the partial results; -1: the item is whole
+};
+
+// One item whose splits the merge kernel joins.
+struct alignas(16) PagedMerge {
+  int tok0, q_len, blk, slot0;
+  int n, pad[3];
+};
+
+struct PagedLayout {
+  size_t first_off, work_off, merge_off, o_off, lse_off, total;
+  int64_t max_work;   // splits of one KV head
+  int64_t max_slots;  // slots of one KV head
+};
+
+// How the rows are cut for a group size, and how far splits go.
+struct PagedShape {
+  bool tiles;      // the tensor-memory kernel (else the register kernel)
+  int rows;        // rows of a block
+  int unit;        // keys of a unit
+  int min_units;   // an item is split only above this many units
+  int ctas;        // a split does at least 1 / ctas of the whole work
+};
+
+struct PagedParams {
+  const __nv_bfloat16 *q, *k_cache, *v_cache;
+  const int *cu_seqlens, *kv_lens, *page_table;
+  int num_seqs, num_heads, num_kv_heads, group;
+  int num_pages, page_shift, max_pages, causal;
+  int max_seqlen, max_kv_len;
+  long long total_q, page_stride;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;  // [total_q, num_heads] or null
+  WsHeader* hdr;
+  int* first;         // [num_seqs + 1]: first item of each sequence
+  PagedWork* work;    // [max_work]
+  PagedMerge* merge;  // [max_slots / 2]
+  float* o_part;      // [max_slots, num_kv_heads, rows, D], normalised
+  float* lse_part;    // [max_slots, num_kv_heads, rows], natural log
+  long long max_work, max_slots;
+  PagedShape shape;
+};
+
+cudaError_t launch_paged_schedule(const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedParams& p, int D, int num_sms, cudaStream_t stream);
 
 }  // namespace cpattn

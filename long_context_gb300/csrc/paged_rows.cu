@@ -1,0 +1,334 @@
+// Attention of few rows over a paged KV cache: one token a sequence, or a few,
+// for every query head that shares a KV head.
+//
+// A CTA (4 warps) has one block of up to 16 or 32 rows of one KV head and one
+// split of the keys.  Its work is HBM bound: a key and its value (4 D bytes)
+// are read once and meet at most 32 rows.  Each warp takes every fourth group
+// of 16 keys on its own: it copies the group's K and V rows into its ring of
+// stages with cp.async (a group never straddles a page, so it needs one page
+// number, read a group ahead), multiplies with 16 x 8 x 16 matrix
+// instructions (the 16 rows of Q in registers are the left operand) and keeps
+// its own softmax state, so the warps never wait for one another until they
+// join their states at the end.  tcgen05 has nothing to give here: its tiles
+// have 64 or 128 rows, of which 16 would be used, and the matrix instructions
+// that 16 rows need take a small part of the time that the bytes take.
+//
+// Softmax: p = 2^(s scale log2 e - m), one pass with a running maximum m that
+// moves only when a group's maximum exceeds it by 8 powers of two (O and l
+// share the reference, so O / l and m + ln l do not depend on it); l sums p in
+// fp32, P is rounded to bf16 for its product with V, O accumulates in fp32.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace cpattn {
+
+namespace {
+
+constexpr int kPrThreads = 128;
+constexpr int kPrWarps = kPrThreads / 32;
+constexpr int kGroupKeys = 16;
+constexpr float kNegInfR = -__builtin_huge_valf();
+constexpr float kLn2R = 0.69314718055994530942f;
+constexpr float kMoveBy = 8.0f;  // powers of two
+
+template <int D>
+struct RowsCfg {
+  static constexpr int kHalf = kGroupKeys * D * 2;  // K (or V) of one group
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kSmem = kPrWarps * kStages * kStage;  // 96 KB: two CTAs a SM
+};
+
+// Byte offset of 16-byte chunk c of row r; the low chunk bits are exchanged
+// with the row's so that ldmatrix reads eight rows without a bank conflict.
+template <int D>
+__device__ __forceinline__ int at(int r, int c) {
+  return r * (D * 2) + ((c ^ (r & 7)) << 4);
+}
+
+}  // namespace
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedParams p) {
+  using C = RowsCfg<D>;
+  constexpr int kRows = 16 * MT;
+  constexpr int kCh = D / 8;         // 16-byte chunks of a row
+  constexpr int kRpi = 32 / kCh;     // rows one warp copy covers
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kPrWarps][kRows], s_l[kPrWarps][kRows];
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int Hk = p.num_kv_heads, G = p.group;
+  const int e = static_cast<int>(blockIdx.x) / Hk;
+  const int h = static_cast<int>(blockIdx.x) - e * Hk;
+  if (e >= __ldcg(&p.hdr->n_items)) return;
+  const int4* wp = reinterpret_cast<const int4*>(p.work + e);
+  const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1);
+  const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
+  const int blk = w1.x, kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
+  // Rows of this block: [row0, row0 + kRows), those below 0 are not there.
+  const int all_rows = q_len * G;
+  const int n_blk = (all_rows + kRows - 1) / kRows;
+  const int row0 = all_rows - (n_blk - blk) * kRows;
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;
+  const int page_mask = (1 << p.page_shift) - 1;
+  const size_t row_pitch = static_cast<size_t>(Hk) * D;
+  const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
+
+  // Groups of this warp: kv_lo / 16 + warp, + 4, ...
+  const int n_groups = (kv_hi - kv_lo + kGroupKeys - 1) / kGroupKeys;
+  const int n = n_groups > warp ? (n_groups - warp + kPrWarps - 1) / kPrWarps : 0;
+  auto group_key = [&](int j) { return kv_lo + (warp + j * kPrWarps) * kGroupKeys; };
+  int next_page = n > 0 ? __ldg(pages + (group_key(0) >> p.page_shift)) : 0;
+  auto copy = [&](int j) {
+    if (j < n) {
+      const int key0 = group_key(j);
+      int page = next_page;
+      if (j + 1 < n) next_page = __ldg(pages + (group_key(j + 1) >> p.page_shift));
+      int last = kv_len;  // keys at or beyond it are filled with zeros
+      if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) atomicCAS(&p.hdr->error, 0, 1);  // CPATTN_ERR_INVALID_ARG
+        page = 0;
+        last = 0;
+      }
+      const int r0 = lane / kCh, c = lane % kCh;
+      const size_t off = static_cast<size_t>(page) * p.page_stride +
+                         static_cast<size_t>((key0 & page_mask) + r0) * row_pitch +
+                         static_cast<size_t>(h) * D + c * 8;
+      const __nv_bfloat16* ks = p.k_cache + off;
+      const __nv_bfloat16* vs = p.v_cache + off;
+      const uint32_t dst = ring + (j % C::kStages) * C::kStage;
+#pragma unroll
+      for (int it = 0; it < kGroupKeys / kRpi; ++it) {
+        const int r = r0 + it * kRpi;
+        const bool in = key0 + r < last;
+        const size_t step = in ? it * kRpi * row_pitch : 0;
+        const __nv_bfloat16* kr = in ? ks + step : p.k_cache;
+        const __nv_bfloat16* vr = in ? vs + step : p.v_cache;
+        cp_async16(dst + at<D>(r, c), kr, in ? 16 : 0);
+        cp_async16(dst + C::kHalf + at<D>(r, c), vr, in ? 16 : 0);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int j = 0; j < C::kStages - 1; ++j) copy(j);
+
+  // Q as left operands: lane l holds rows l / 4 and l / 4 + 8, columns
+  // 2 (l % 4) + {0, 1} and + 8 of each 16 x 16 block.
+  uint32_t qa[MT][D / 16][4];
+  int lim[MT][2];  // keys below it are visible
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int row = row0 + mt * 16 + hf * 8 + (lane >> 2);
+      const bool in = row >= 0;
+      const int tok = in ? row / G : 0;
+      lim[mt][hf] = in ? (p.causal ? kv_len - q_len + tok + 1 : kv_len) : 0;
+      const __nv_bfloat16* src =
+          p.q + (static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (in ? row - tok * G : 0)) * D +
+          2 * (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qa[mt][kk][hf] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16)) : 0u;
+        qa[mt][kk][hf + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8)) : 0u;
+      }
+    }
+  // Groups ending at or below this key need no mask (rows are in order, so
+  // the block's first row sees the fewest keys).
+  const int first_tok = max(row0, 0) / G;
+  const int free_end = row0 < 0 ? 0 : (p.causal ? kv_len - q_len + first_tok + 1 : kv_len);
+
+  float o[MT][D / 8][4];
+  float m[MT][2], l[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt][0] = m[mt][1] = kNegInfR;
+    l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+    for (int f = 0; f < D / 8; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[mt][f][i] = 0.f;
+  }
+
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    cp_async_wait<C::kStages - 2>();
+    __syncwarp();
+    copy(j + C::kStages - 1);
+    const uint32_t kb = ring + (j % C::kStages) * C::kStage;
+    const uint32_t vb = kb + C::kHalf;
+    float s[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t b[4];
+      ldmatrix4(kb + at<D>((lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), b);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma_16816(s[mt][0], qa[mt][kk], b[0], b[1]);
+        mma_16816(s[mt][1], qa[mt][kk], b[2], b[3]);
+      }
+    }
+    const int key0 = group_key(j);
+    if (key0 + kGroupKeys > free_end) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = key0 + (i >> 2) * 8 + 2 * (lane & 3) + (i & 1);
+          if (key >= lim[mt][(i >> 1) & 1]) s[mt][i >> 2][i & 3] = kNegInfR;
+        }
+    }
+    bool move = false;
+    float top[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float t = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
+                        fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        top[mt][hf] = t * p.scale_log2;
+        move = move || top[mt][hf] > m[mt][hf] + kMoveBy;
+      }
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float mn = fmaxf(m[mt][hf], top[mt][hf]);
+          const float alpha = m[mt][hf] == kNegInfR ? 0.f : ex2_approx(m[mt][hf] - mn);
+          m[mt][hf] = mn;
+          l[mt][hf] *= alpha;
+#pragma unroll
+          for (int f = 0; f < D / 8; ++f) {
+            o[mt][f][2 * hf] *= alpha;
+            o[mt][f][2 * hf + 1] *= alpha;
+          }
+        }
+    }
+    uint32_t pa[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float ref = m[mt][hf] == kNegInfR ? 0.f : m[mt][hf];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = ex2_approx(fmaf(s[mt][t][2 * hf], p.scale_log2, -ref));
+          const float p1 = ex2_approx(fmaf(s[mt][t][2 * hf + 1], p.scale_log2, -ref));
+          l[mt][hf] += p0 + p1;
+          pa[mt][2 * t + hf] = pack_bf16x2(p0, p1);
+        }
+      }
+#pragma unroll
+    for (int f = 0; f < D / 16; ++f) {
+      uint32_t b[4];
+      ldmatrix4_trans(vb + at<D>((lane & 7) + (((lane >> 3) & 1) << 3), f * 2 + (lane >> 4)), b);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma_16816(o[mt][2 * f], pa[mt], b[0], b[1]);
+        mma_16816(o[mt][2 * f + 1], pa[mt], b[2], b[3]);
+      }
+    }
+  }
+
+  // Join the warps' states (their rings are done with) and write the rows.
+  cp_async_wait<0>();
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(smem) + warp * kRows * D;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = mt * 16 + hf * 8 + (lane >> 2);
+      float sum = l[mt][hf];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if ((lane & 3) == 0) {
+        s_m[warp][r] = m[mt][hf];
+        s_l[warp][r] = sum;
+      }
+#pragma unroll
+      for (int f = 0; f < D / 8; ++f)
+        *reinterpret_cast<float2*>(so + r * D + f * 8 + 2 * (lane & 3)) =
+            make_float2(o[mt][f][2 * hf], o[mt][f][2 * hf + 1]);
+    }
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(smem);
+  for (int x = threadIdx.x; x < kRows * (D / 4); x += kPrThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+    const int row = row0 + r;
+    if (row < 0) continue;
+    float top = kNegInfR;
+#pragma unroll
+    for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, s_m[w][r]);
+    float den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kPrWarps; ++w) {
+      // A warp without a visible key has l = 0 and O = 0 (or NaN in both, which
+      // the row then shows).
+      const float f = s_m[w][r] == kNegInfR ? 1.f : ex2_approx(s_m[w][r] - top);
+      den = fmaf(f, s_l[w][r], den);
+      const float4 v = *reinterpret_cast<const float4*>(all + (w * kRows + r) * D + c);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float ref = top == kNegInfR ? 0.f : top;
+    const float lse = den == 0.f ? kNegInfR : (ref + __log2f(den)) * kLn2R;
+    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (slot >= 0) {
+      const size_t part = (static_cast<size_t>(slot) * Hk + h) * kRows + r;
+      *reinterpret_cast<float4*>(p.o_part + part * D + c) = acc;
+      if (c == 0) p.lse_part[part] = lse;
+    } else {
+      const int tok = row / G;
+      const size_t at_row = static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (row - tok * G);
+      *reinterpret_cast<uint2*>(p.out + at_row * D + c) =
+          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      if (c == 0 && p.lse != nullptr) p.lse[at_row] = lse;
+    }
+  }
+}
+
+template <int D, int MT>
+static cudaError_t launch_paged_rows_t(const PagedParams& p, cudaStream_t stream) {
+  auto kern = paged_rows_kernel<D, MT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             RowsCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.max_work * p.num_kv_heads));
+  cfg.blockDim = dim3(kPrThreads);
+  cfg.dynamicSmemBytes = RowsCfg<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream) {
+  if (p.shape.rows == 16)
+    return D == 64 ? launch_paged_rows_t<64, 1>(p, stream) : launch_paged_rows_t<128, 1>(p, stream);
+  return D == 64 ? launch_paged_rows_t<64, 2>(p, stream) : launch_paged_rows_t<128, 2>(p, stream);
+}
+
+}  // namespace cpattn

@@ -40,6 +40,12 @@ Modules:
   against its sharded KV cache, with the LSE-form merge of the shards.
 * :mod:`oracle.ulysses`   -- the Ulysses all-to-all as a head-group layout
   transform, and attention run per head group.
+* :mod:`oracle.norm_rope` -- RMS norm and rotary position embedding of query
+  and key heads, and their gradients (no page describes them: written from the
+  definition in ``include/cpattn.h``).
+* :mod:`oracle.paged`     -- the paged KV cache: where a token stands, and
+  attention of new tokens over it (likewise).
 """
 
-from . import attention, backward, dcp, decode, planner, ulysses  # noqa: F401
+from . import (attention, backward, dcp, decode, norm_rope, paged, planner,  # noqa: F401
+               ulysses)
