@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libcpattn.so")
 
 SOURCES = ["plan.cpp", "api.cu", "schedule.cu", "merge.cu", "attn_fwd.cu", "attn_bwd.cu",
            "dcp.cu", "decode.cu", "noalloc.cu", "ulysses.cu", "norm_rope.cu", "paged_sched.cu",
-           "paged_rows.cu", "serve_api.cu"]
+           "paged_rows.cu", "paged_tile.cu", "serve_api.cu"]
 HEADERS = ["kernels.h", "ptx.cuh", "work.cuh", "debug.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

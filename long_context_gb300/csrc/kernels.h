@@ -140,6 +140,12 @@ struct DeviceInfo {
 // Properties of the current device (cached); a cpattn_status.
 int device_info(DeviceInfo* out);
 
+// Tensor map over a bf16 array of `rank` dimensions (innermost first; strides
+// in bytes from the second on), 128-byte swizzle; a cpattn_status.  Needs an
+// earlier device_info call.
+int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box);
+
 // Host-checkable argument rules of the forward calls; a cpattn_status.
 int check_fwd(const FwdArgs& a);
 
@@ -300,6 +306,9 @@ struct PagedParams {
 
 cudaError_t launch_paged_schedule(const PagedParams& p, cudaStream_t stream);
 cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream);
+cudaError_t launch_paged_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& to, const PagedParams& p, int D,
+                              cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedParams& p, int D, int num_sms, cudaStream_t stream);
 
 }  // namespace cpattn

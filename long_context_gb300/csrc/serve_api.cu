@@ -57,12 +57,46 @@ int page_shift_of(int32_t page_size) {
 
 PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
   PagedShape s;
-  s.tiles = false;
-  s.rows = group * max_seqlen <= 16 ? 16 : 32;
-  s.unit = 64;
-  s.min_units = 1;
-  s.ctas = 608;
+  const int64_t rows = group * max_seqlen;
+  s.tiles = rows > 32;
+  if (s.tiles) {
+    s.rows = kNQ * static_cast<int>(kBM / group * group);
+    s.unit = kBN;
+    s.min_units = 8;
+    s.ctas = 304;
+  } else {
+    s.rows = rows <= 16 ? 16 : 32;
+    s.unit = 64;
+    s.min_units = 1;
+    s.ctas = 608;
+  }
   return s;
+}
+
+// Q or O: [T, H, D] in boxes of 64 features x one KV head's query heads x a Q
+// tile's tokens.
+int q_tile_map(CUtensorMap* map, const void* base, const PagedParams& p, int D) {
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.num_heads),
+                              static_cast<cuuint64_t>(p.total_q)};
+  const cuuint64_t strides[2] = {row, row * p.num_heads};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group),
+                             static_cast<cuuint32_t>(p.shape.rows / (kNQ * p.group))};
+  return encode_bf16_map(map, base, 3, dims, strides, box);
+}
+
+// A cache: [pages, page size, KV heads, D] in boxes of 64 features x one head
+// x a page's rows (at most a key tile's).
+int cache_map(CUtensorMap* map, const void* base, const PagedParams& p, int D) {
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const int size = 1 << p.page_shift;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.num_kv_heads),
+                              static_cast<cuuint64_t>(size),
+                              static_cast<cuuint64_t>(p.num_pages)};
+  const cuuint64_t strides[3] = {row, row * p.num_kv_heads,
+                                 static_cast<cuuint64_t>(p.page_stride) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(size < kBN ? size : kBN), 1};
+  return encode_bf16_map(map, base, 4, dims, strides, box);
 }
 
 PagedLayout paged_layout(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t D,
@@ -394,7 +428,17 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_paged_schedule(p, s) != cudaSuccess) return CPATTN_ERR_CUDA;
   if (!any) return CPATTN_OK;
-  if (launch_paged_rows(p, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+  if (p.shape.tiles) {
+    CUtensorMap tq, tk, tv, to;
+    if (q_tile_map(&tq, q, p, head_dim) != CPATTN_OK ||
+        q_tile_map(&to, out, p, head_dim) != CPATTN_OK ||
+        cache_map(&tk, k_cache, p, head_dim) != CPATTN_OK ||
+        cache_map(&tv, v_cache, p, head_dim) != CPATTN_OK)
+      return CPATTN_ERR_CUDA;
+    if (launch_paged_tile(tq, tk, tv, to, p, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+  } else if (launch_paged_rows(p, head_dim, s) != cudaSuccess) {
+    return CPATTN_ERR_CUDA;
+  }
   // An item of no more than min_units units is never split.
   if (max_kv_len > p.shape.min_units * p.shape.unit &&
       launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
