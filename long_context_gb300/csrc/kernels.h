@@ -224,7 +224,7 @@ struct NormRopeParams {
   long long page_stride;
 };
 
-cudaError_t launch_norm_rope(const NormRopeParams& p, int D, bool interleaved,
+cudaError_t launch_norm_rope(const NormRopeParams& p, int D, bool interleaved, int num_sms,
                              cudaStream_t stream);
 
 constexpr int kNormRopeBwdCtas = 1024;  // at most this many rows of partial weight gradients

@@ -12,42 +12,39 @@
 //   dw = sum over rows of g hat,  u = g w,  dx = r (u - hat mean(u hat)).
 //
 // HBM bound: a row is read once and written once (the backward reads two rows
-// and writes one).  D / 8 lanes own a row, 16 bytes each, so the mean is a few
-// shuffles inside the row's lanes and a half-split pair is one shuffle away;
-// everything between the load and the store is fp32 in registers, rounded to
-// bf16 once.  A lane group takes kUnit heads of one token at a time: their
-// loads are in flight together and share the position's cos and sin, which
-// are the only loads that depend on another load.
+// and writes one).  D / 8 lanes own a row.  The rows reach shared memory by
+// 16-byte asynchronous copies, so that many are in flight without registers;
+// from there a lane takes both members of its pairs, four features at its two
+// places (4 c and R/2 + 4 c for lane c of a half-split rotation, else 8 c and
+// 8 c + 4), so no value passes between lanes but the mean's partial sums.
+// Everything between the load and the store is fp32 in registers, in packed
+// pairs, rounded to bf16 once.
 #include <cuda_bf16.h>
+#include <cstdlib>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace cpattn {
 
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kUnit = 4;     // heads of one token a lane group has in flight
-constexpr int kBwdUnit = 2;  // backward: two rows (x, dy) per head
+constexpr int kUnit = 4;     // heads of one batch of copies
+constexpr int kBwdUnit = 4;  // backward
+constexpr int kBwdSmem = 2 * 2 * kBwdUnit * kNrThreads * 16;
 constexpr int kErrArg = 1;   // CPATTN_ERR_INVALID_ARG
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = __bfloat1622float2(h[e]);
-    f[2 * e] = t.x;
-    f[2 * e + 1] = t.y;
-  }
+// Four bf16 values as two packed pairs of floats.
+__device__ __forceinline__ void unpack4(const uint2& u, float2* f) {
+  f[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+  f[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
-
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  uint4 u;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-  return u;
+__device__ __forceinline__ uint2 pack4(const float2* f) {
+  return make_uint2(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y));
 }
+__device__ __forceinline__ float2 swap2(const float2& v) { return make_float2(v.y, v.x); }
+__device__ __forceinline__ float2 both2(float v) { return make_float2(v, v); }
 
 // Sum over the lanes of a row (groups of LG lanes never straddle a warp).
 template <int LG>
@@ -57,78 +54,64 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// The rotation's coefficients for the 8 features of lane chunk c:
-// y_e = n_e cs[e] + partner_e sn[e], the sign of the sine folded into sn.
-// `partner_lane` is the lane (of the warp) that holds the partner features
-// (half split); chunks at or beyond R take no part.
+// A lane's features are a (four at `lo`) and b (four at `hi`):
+//   y_a = a ac + a' as,  y_b = b bc + b' bs,
+// where a', b' are the pairs' other members: b and a (half split), or a and b
+// with their pairs swapped (interleaved).
 struct Turn {
-  float cs[8], sn[8];
-  int partner_lane;
-  bool on;
+  float2 ac[2], as[2], bc[2], bs[2];
+  int lo, hi;
+  bool on;  // the lane's features turn
 };
 
+__device__ __forceinline__ void place_lane(Turn& t, int c, int rot, bool interleaved) {
+  t.on = c < (rot >> 3);
+  const bool apart = t.on && !interleaved;
+  t.lo = apart ? 4 * c : 8 * c;
+  t.hi = apart ? (rot >> 1) + 4 * c : 8 * c + 4;
+}
+
+// Coefficients of the position whose table row is `row` (valid: the row may be
+// read); `sgn` is 1 for the rotation and -1 for its inverse.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void load_turn(Turn& t, const float* row, int rot, int c, int lane,
-                                          bool valid) {
-  const int f0 = c * 8, half = rot >> 1;
-  t.on = f0 < rot;
-  t.partner_lane = lane;
+__device__ __forceinline__ void load_turn(Turn& t, const float* row, int rot, int c, bool valid,
+                                          float sgn) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    t.cs[e] = 1.f;
-    t.sn[e] = 0.f;
+  for (int i = 0; i < 2; ++i) {
+    t.ac[i] = t.bc[i] = both2(1.f);
+    t.as[i] = t.bs[i] = both2(0.f);
   }
-  if (!t.on) return;
-  if (INTERLEAVED) {
-    if (valid) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(row + (f0 >> 1)));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + (f0 >> 1)));
-      const float cc[4] = {cv.x, cv.y, cv.z, cv.w};
-      const float ss[4] = {sv.x, sv.y, sv.z, sv.w};
+  if (!t.on || !valid) return;
+  const float4 cv = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
+  const float4 sv = __ldg(reinterpret_cast<const float4*>(row + (rot >> 1) + 4 * c));
+  const float cs[4] = {cv.x, cv.y, cv.z, cv.w};
+  const float sn[4] = {sgn * sv.x, sgn * sv.y, sgn * sv.z, sgn * sv.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        t.cs[2 * e] = t.cs[2 * e + 1] = cc[e];
-        t.sn[2 * e] = -ss[e];
-        t.sn[2 * e + 1] = ss[e];
-      }
-    }
-  } else {
-    const bool first = f0 < half;
-    const int j0 = first ? f0 : f0 - half;
-    t.partner_lane = first ? lane + (half >> 3) : lane - (half >> 3);
-    if (valid) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + j0) + q);
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + j0) + q);
-        t.cs[4 * q] = cv.x;
-        t.cs[4 * q + 1] = cv.y;
-        t.cs[4 * q + 2] = cv.z;
-        t.cs[4 * q + 3] = cv.w;
-        t.sn[4 * q] = first ? -sv.x : sv.x;
-        t.sn[4 * q + 1] = first ? -sv.y : sv.y;
-        t.sn[4 * q + 2] = first ? -sv.z : sv.z;
-        t.sn[4 * q + 3] = first ? -sv.w : sv.w;
-      }
+  for (int i = 0; i < 2; ++i) {
+    if (INTERLEAVED) {
+      t.ac[i] = both2(cs[i]);
+      t.as[i] = make_float2(-sn[i], sn[i]);
+      t.bc[i] = both2(cs[2 + i]);
+      t.bs[i] = make_float2(-sn[2 + i], sn[2 + i]);
+    } else {
+      t.ac[i] = t.bc[i] = make_float2(cs[2 * i], cs[2 * i + 1]);
+      t.as[i] = make_float2(-sn[2 * i], -sn[2 * i + 1]);
+      t.bs[i] = make_float2(sn[2 * i], sn[2 * i + 1]);
     }
   }
 }
 
-// n -> y in place; `sgn` is 1 for the rotation and -1 for its inverse.  Every
-// lane of the warp executes it (the partner exchange is a shuffle).
 template <bool INTERLEAVED>
-__device__ __forceinline__ void apply_turn(const Turn& t, float* n, float sgn) {
-  float pn[8];
-  if (INTERLEAVED) {
+__device__ __forceinline__ void apply_turn(const Turn& t, float2* a, float2* b) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) pn[e] = n[e ^ 1];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) pn[e] = __shfl_sync(0xffffffffu, n[e], t.partner_lane);
-  }
-  if (t.on) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) n[e] = n[e] * t.cs[e] + pn[e] * (sgn * t.sn[e]);
+  for (int i = 0; i < 2; ++i) {
+    const float2 pa = INTERLEAVED ? swap2(a[i]) : b[i];
+    const float2 pb = INTERLEAVED ? swap2(b[i]) : a[i];
+    const float2 ya = __fmul2_rn(a[i], t.ac[i]), yb = __fmul2_rn(b[i], t.bc[i]);
+    // Features that do not turn take no product with a partner (0 times an
+    // infinity).
+    a[i] = t.on ? __ffma2_rn(pa, t.as[i], ya) : ya;
+    b[i] = t.on ? __ffma2_rn(pb, t.bs[i], yb) : yb;
   }
 }
 
@@ -156,14 +139,16 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t, int c, int 
 
 }  // namespace
 
-template <int D, bool INTERLEAVED, bool PAGED>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
+template <int D, bool INTERLEAVED, bool PAGED, int NB>
+__global__ void __launch_bounds__(kNrThreads, PAGED ? 4 : 5) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LG = D / 8;
+  constexpr int run = NB * kUnit;  // heads of a unit
+  extern __shared__ __align__(16) uint8_t ring[];  // [run][threads] pieces of 16 bytes
   constexpr int kGroups = kNrThreads / LG;
   const int lane = threadIdx.x & 31;
   const int c = lane % LG;
-  const int uq = (p.q_heads + kUnit - 1) / kUnit;
-  const int uk = (p.kv_heads + kUnit - 1) / kUnit;
+  const int uq = (p.q_heads + run - 1) / run;
+  const int uk = (p.kv_heads + run - 1) / run;
   const int upt = uq + (PAGED ? 2 : 1) * uk;  // units of a token
   const long long unit = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / LG;
   const bool live = unit < p.total_tokens * upt;
@@ -172,18 +157,21 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
   // Which of q (0), k (1), v (2) this unit belongs to.
   const int which = hu < uq ? 0 : (hu < uq + uk ? 1 : 2);
   hu -= which == 0 ? 0 : (which == 1 ? uq : uq + uk);
-  const int h0 = hu * kUnit;
-  const int heads = which == 0 ? p.q_heads : p.kv_heads;
+  const int h0 = hu * run;
+  const int heads = live ? min(h0 + run, which == 0 ? p.q_heads : p.kv_heads) : 0;
   const __nv_bfloat16* in =
       (which == 0 ? p.q : which == 1 ? p.k : p.v) +
       static_cast<size_t>(token) *
           (which == 0 ? p.q_stride : which == 1 ? p.k_stride : p.v_stride);
-  uint4 x[kUnit];
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
 #pragma unroll
-  for (int u = 0; u < kUnit; ++u) {
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (live && h0 + u < heads)
-      x[u] = __ldcs(reinterpret_cast<const uint4*>(in + static_cast<size_t>(h0 + u) * D) + c);
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      const int i = nb * kUnit + u;
+      if (h0 + i < heads) cp_async16(mine + i * (kNrThreads * 16), in + (h0 + i) * D + c * 8, 16);
+    }
+    cp_async_commit();
   }
 
   bool ok = live;
@@ -225,39 +213,60 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
           static_cast<size_t>(token) * (which == 0 ? p.q_out_stride : p.k_out_stride);
   }
 
-  if (PAGED && __all_sync(0xffffffffu, which == 2 || !ok)) {
-    // A warp of values alone: copied as they are.
-#pragma unroll
-    for (int u = 0; u < kUnit; ++u)
-      if (ok && h0 + u < heads)
-        *(reinterpret_cast<uint4*>(out + static_cast<size_t>(h0 + u) * D) + c) = x[u];
-    return;
-  }
-
   Turn t;
   const bool turning = p.table != nullptr;
-  if (turning)
-    load_turn<INTERLEAVED>(t, p.table + static_cast<size_t>(ok ? pos : 0) * p.rot, p.rot, c, lane,
-                           ok);
+  const bool plain = PAGED && which == 2;  // values are copied as they are
+  place_lane(t, c, turning ? p.rot : 0, INTERLEAVED);
+  load_turn<INTERLEAVED>(t, p.table + static_cast<size_t>(ok ? pos : 0) * p.rot, p.rot, c,
+                         ok && !plain, 1.f);
+  // The weights go into the rotation's coefficients: with n = x r w,
+  // y = r (x (w cos) + x' (w' sin)).
   const __nv_bfloat16* wp = which == 0 ? p.q_weight : p.k_weight;
-  float w[8];
-  if (wp != nullptr) unpack8(__ldg(reinterpret_cast<const uint4*>(wp) + c), w);
+  const bool normed = wp != nullptr;  // the same for every lane: both weights or no queries
+  if (normed) {
+    float2 wa[2], wb[2];
+    unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.lo)), wa);
+    unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.hi)), wb);
 #pragma unroll
-  for (int u = 0; u < kUnit; ++u) {
-    float n[8];
-    unpack8(x[u], n);
-    if (wp != nullptr) {  // the same for every lane: both weights or no queries
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(n[e], n[e], ss);
-      const float r = rsqrtf(row_sum<LG>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] = n[e] * r * w[e];
+    for (int i = 0; i < 2; ++i) {
+      t.ac[i] = __fmul2_rn(t.ac[i], wa[i]);
+      t.bc[i] = __fmul2_rn(t.bc[i], wb[i]);
+      t.as[i] = __fmul2_rn(t.as[i], INTERLEAVED ? swap2(wa[i]) : wb[i]);
+      t.bs[i] = __fmul2_rn(t.bs[i], INTERLEAVED ? swap2(wb[i]) : wa[i]);
     }
-    if (turning) apply_turn<INTERLEAVED>(t, n, 1.f);
-    if (ok && h0 + u < heads)
-      *(reinterpret_cast<uint4*>(out + static_cast<size_t>(h0 + u) * D) + c) =
-          (PAGED && which == 2) ? x[u] : pack8(n);
+  }
+  const uint8_t* row = ring + (threadIdx.x - c) * 16;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    // This batch's rows have landed, every lane's part of them.
+    if (nb == 0) cp_async_wait<NB - 1>(); else cp_async_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      const int i = nb * kUnit + u, h = h0 + i;
+      const uint2 xa = *reinterpret_cast<const uint2*>(row + i * (kNrThreads * 16) + t.lo * 2);
+      const uint2 xb = *reinterpret_cast<const uint2*>(row + i * (kNrThreads * 16) + t.hi * 2);
+      float2 a[2], b[2];
+      unpack4(xa, a);
+      unpack4(xb, b);
+      if (normed) {
+        float2 ss = __fmul2_rn(a[0], a[0]);
+        ss = __ffma2_rn(a[1], a[1], ss);
+        ss = __ffma2_rn(b[0], b[0], ss);
+        ss = __ffma2_rn(b[1], b[1], ss);
+        const float2 r = both2(rsqrtf(row_sum<LG>(ss.x + ss.y) * (1.f / D) + p.eps));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          a[k] = __fmul2_rn(a[k], r);
+          b[k] = __fmul2_rn(b[k], r);
+        }
+      }
+      apply_turn<INTERLEAVED>(t, a, b);
+      if (ok && h < heads) {
+        *reinterpret_cast<uint2*>(out + h * D + t.lo) = plain ? xa : pack4(a);
+        *reinterpret_cast<uint2*>(out + h * D + t.hi) = plain ? xb : pack4(b);
+      }
+    }
   }
 }
 
@@ -270,7 +279,8 @@ template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int LG = D / 8;
   constexpr int kGroups = kNrThreads / LG;
-  __shared__ float red[kGroups][D];
+  extern __shared__ __align__(16) uint8_t ring[];  // [2][gradients, inputs][kBwdUnit][threads] x 16
+  __shared__ __align__(16) float red[kGroups][D];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int c = lane % LG;
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
   const int cta = static_cast<int>(blockIdx.x) - (is_k ? p.q_ctas : 0);
   const int ctas = is_k ? static_cast<int>(gridDim.x) - p.q_ctas : p.q_ctas;
   const int heads = is_k ? p.kv_heads : p.q_heads;
-  const int upt = (heads + kBwdUnit - 1) / kBwdUnit;
+  const int upt = (heads + kBwdUnit - 1) / kBwdUnit;  // units of a token
   const long long units = p.total_tokens * upt;
   const __nv_bfloat16* xin = is_k ? p.k : p.q;
   const __nv_bfloat16* gin = is_k ? p.dk_out : p.dq_out;
@@ -289,74 +299,120 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
   const long long o_stride = is_k ? p.dk_stride : p.dq_stride;
   const bool normed = p.q_weight != nullptr;
   const bool turning = p.table != nullptr;
-  float w[8], dw[8];
+  Turn t;
+  place_lane(t, c, turning ? p.rot : 0, INTERLEAVED);
+  float2 wa[2], wb[2], dwa[2], dwb[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dw[e] = 0.f;
-  if (normed) unpack8(__ldg(reinterpret_cast<const uint4*>(is_k ? p.k_weight : p.q_weight) + c), w);
+  for (int i = 0; i < 2; ++i) wa[i] = wb[i] = dwa[i] = dwb[i] = both2(0.f);
+  if (normed) {
+    const __nv_bfloat16* wp = is_k ? p.k_weight : p.q_weight;
+    unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.lo)), wa);
+    unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.hi)), wb);
+  }
   const long long stride = static_cast<long long>(ctas) * kGroups;
-  // Whole warps stay in the loop together (the shuffles are warp-wide).
-  for (long long base = static_cast<long long>(cta) * kGroups; base < units; base += stride) {
-    const long long unit = base + group;
-    const bool live = unit < units;
-    const int token = live ? static_cast<int>(static_cast<unsigned>(unit) / upt) : 0;
-    const int h0 =
-        live ? static_cast<int>(static_cast<unsigned>(unit) - token * upt) * kBwdUnit : 0;
-    const __nv_bfloat16* xt = xin + token * x_stride;
-    const __nv_bfloat16* gt = gin + token * g_stride;
-    uint4 xr[kBwdUnit], gr[kBwdUnit];
+  // A unit is kBwdUnit heads of one token.  The next unit's rows are copied
+  // to shared memory while the current unit's are used.  Whole warps stay in the loop together (the shuffles are warp-wide).
+  struct Place {
+    int token, h0, end, pos;
+  };
+  auto place = [&](long long u) {
+    Place a = {0, 0, 0, 0};
+    if (u < units) {
+      a.token = static_cast<int>(static_cast<unsigned>(u) / upt);
+      a.h0 = static_cast<int>(static_cast<unsigned>(u) - a.token * upt) * kBwdUnit;
+      a.end = min(a.h0 + kBwdUnit, heads);
+      if (turning) a.pos = __ldg(p.positions + a.token);
+    }
+    return a;
+  };
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint8_t* row = ring + (threadIdx.x - c) * 16;
+  auto load = [&](const Place& a, int buf) {
 #pragma unroll
     for (int u = 0; u < kBwdUnit; ++u) {
-      xr[u] = gr[u] = make_uint4(0, 0, 0, 0);
-      if (live && h0 + u < heads) {
-        gr[u] = __ldcs(reinterpret_cast<const uint4*>(gt + static_cast<size_t>(h0 + u) * D) + c);
+      const int h = a.h0 + u;
+      const uint32_t dst = mine + (buf * 2 * kBwdUnit + u) * (kNrThreads * 16);
+      if (h < a.end) {
+        cp_async16(dst, gin + a.token * g_stride + h * D + c * 8, 16);
         if (normed)
-          xr[u] = __ldcs(reinterpret_cast<const uint4*>(xt + static_cast<size_t>(h0 + u) * D) + c);
+          cp_async16(dst + kBwdUnit * (kNrThreads * 16), xin + a.token * x_stride + h * D + c * 8,
+                     16);
       }
     }
-    bool ok = live;
-    Turn t;
+    cp_async_commit();
+  };
+  long long unit = static_cast<long long>(cta) * kGroups + group;
+  Place at = place(unit);
+  load(at, 0);
+  int buf = 0;
+  for (long long base = static_cast<long long>(cta) * kGroups; base < units; base += stride) {
+    unit += stride;
+    const Place ahead = place(unit);
+    load(ahead, buf ^ 1);
+    bool ok = at.end > 0;
     if (turning) {
-      const int pos = live ? __ldg(p.positions + token) : 0;
-      const bool good = pos >= 0 && pos < p.max_pos;
-      if (live && !good && p.status != nullptr && c == 0) atomicCAS(p.status, 0, kErrArg);
+      const bool good = at.pos >= 0 && at.pos < p.max_pos;
+      if (ok && !good && p.status != nullptr && c == 0) atomicCAS(p.status, 0, kErrArg);
       ok = ok && good;
-      load_turn<INTERLEAVED>(t, p.table + static_cast<size_t>(ok ? pos : 0) * p.rot, p.rot, c,
-                             lane, ok);
     }
+    load_turn<INTERLEAVED>(t, p.table + static_cast<size_t>(ok ? at.pos : 0) * p.rot, p.rot, c, ok,
+                           -1.f);
+    cp_async_wait<1>();
+    __syncwarp();
 #pragma unroll
     for (int u = 0; u < kBwdUnit; ++u) {
-      const bool count = ok && h0 + u < heads;
-      float g[8];
-      unpack8(gr[u], g);
-      if (turning) apply_turn<INTERLEAVED>(t, g, -1.f);
+      const int h = at.h0 + u;
+      const bool count = ok && h < at.end;
+      const uint8_t* piece = row + (buf * 2 * kBwdUnit + u) * (kNrThreads * 16);
+      float2 a[2], b[2];
+      unpack4(*reinterpret_cast<const uint2*>(piece + t.lo * 2), a);
+      unpack4(*reinterpret_cast<const uint2*>(piece + t.hi * 2), b);
+      apply_turn<INTERLEAVED>(t, a, b);  // g
       if (normed) {
-        float x[8];
-        unpack8(xr[u], x);
-        float ss = 0.f, dot = 0.f;
+        const uint8_t* px = piece + kBwdUnit * (kNrThreads * 16);
+        float2 xa[2], xb[2];
+        unpack4(*reinterpret_cast<const uint2*>(px + t.lo * 2), xa);
+        unpack4(*reinterpret_cast<const uint2*>(px + t.hi * 2), xb);
+        float2 ss = both2(0.f), dot = both2(0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(x[e], x[e], ss);
-          dot = fmaf(g[e] * w[e], x[e], dot);
+        for (int k = 0; k < 2; ++k) {
+          ss = __ffma2_rn(xa[k], xa[k], ss);
+          ss = __ffma2_rn(xb[k], xb[k], ss);
+          dot = __ffma2_rn(__fmul2_rn(a[k], wa[k]), xa[k], dot);
+          dot = __ffma2_rn(__fmul2_rn(b[k], wb[k]), xb[k], dot);
         }
-        ss = row_sum<LG>(ss);
-        dot = row_sum<LG>(dot);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const float m = dot * r * (1.f / D);  // mean(u hat)
+        const float sum = row_sum<LG>(ss.x + ss.y);
+        const float prod = row_sum<LG>(dot.x + dot.y);
+        const float r = rsqrtf(sum * (1.f / D) + p.eps);
+        const float2 r2 = both2(r);
+        const float2 m2 = both2(-prod * r * (1.f / D));  // -mean(u hat)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float hat = x[e] * r;
-          if (count) dw[e] = fmaf(g[e], hat, dw[e]);
-          g[e] = r * (g[e] * w[e] - hat * m);
+        for (int k = 0; k < 2; ++k) {
+          const float2 ha = __fmul2_rn(xa[k], r2), hb = __fmul2_rn(xb[k], r2);
+          if (count) {
+            dwa[k] = __ffma2_rn(a[k], ha, dwa[k]);
+            dwb[k] = __ffma2_rn(b[k], hb, dwb[k]);
+          }
+          a[k] = __fmul2_rn(__ffma2_rn(ha, m2, __fmul2_rn(a[k], wa[k])), r2);
+          b[k] = __fmul2_rn(__ffma2_rn(hb, m2, __fmul2_rn(b[k], wb[k])), r2);
         }
       }
-      if (count)
-        *(reinterpret_cast<uint4*>(out + token * o_stride + static_cast<size_t>(h0 + u) * D) + c) =
-            pack8(g);
+      if (count) {
+        __nv_bfloat16* dst = out + at.token * o_stride + h * D;
+        *reinterpret_cast<uint2*>(dst + t.lo) = pack4(a);
+        *reinterpret_cast<uint2*>(dst + t.hi) = pack4(b);
+      }
     }
+    __syncwarp();  // the buffer is refilled by all lanes
+    at = ahead;
+    buf ^= 1;
   }
   if (!normed) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[group][c * 8 + e] = dw[e];
+  for (int k = 0; k < 2; ++k) {
+    *reinterpret_cast<float2*>(&red[group][t.lo + 2 * k]) = dwa[k];
+    *reinterpret_cast<float2*>(&red[group][t.hi + 2 * k]) = dwb[k];
+  }
   __syncthreads();
   for (int f = threadIdx.x; f < D; f += kNrThreads) {
     float s = 0.f;
@@ -391,36 +447,57 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int D>
-static cudaError_t launch_norm_rope_d(const NormRopeParams& p, bool interleaved,
+template <int D, int NB>
+static cudaError_t launch_norm_rope_t(const NormRopeParams& p, bool interleaved, long long units,
                                       cudaStream_t stream) {
-  const bool paged = p.page_table != nullptr;
-  const long long uq = (p.q_heads + kUnit - 1) / kUnit, uk = (p.kv_heads + kUnit - 1) / kUnit;
-  const long long units = p.total_tokens * (uq + (paged ? 2 : 1) * uk);
   const int groups = kNrThreads / (D / 8);
   const unsigned grid = static_cast<unsigned>((units + groups - 1) / groups);
-  if (grid == 0) return cudaSuccess;
-  if (paged) {
-    if (interleaved) norm_rope_kernel<D, true, true><<<grid, kNrThreads, 0, stream>>>(p);
-    else norm_rope_kernel<D, false, true><<<grid, kNrThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved) norm_rope_kernel<D, true, false><<<grid, kNrThreads, 0, stream>>>(p);
-    else norm_rope_kernel<D, false, false><<<grid, kNrThreads, 0, stream>>>(p);
+  constexpr int kSmem = NB * kUnit * kNrThreads * 16;
+  const bool paged = p.page_table != nullptr;
+  auto kern = paged ? (interleaved ? norm_rope_kernel<D, true, true, NB>
+                                   : norm_rope_kernel<D, false, true, NB>)
+                    : (interleaved ? norm_rope_kernel<D, true, false, NB>
+                                   : norm_rope_kernel<D, false, false, NB>);
+  if (kSmem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
   }
+  kern<<<grid, kNrThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_rope(const NormRopeParams& p, int D, bool interleaved,
+template <int D>
+static cudaError_t launch_norm_rope_d(const NormRopeParams& p, bool interleaved, int num_sms,
+                                      cudaStream_t stream) {
+  auto units_at = [&](int run) {
+    const long long uq = (p.q_heads + run - 1) / run, uk = (p.kv_heads + run - 1) / run;
+    return p.total_tokens * (uq + (p.page_table != nullptr ? 2 : 1) * uk);
+  };
+  // Longer runs of heads share a position's angles and have more loads in
+  // flight, as long as they leave every SM several rounds of CTAs.
+  const long long many = 12LL * num_sms * (kNrThreads / (D / 8));
+  if (units_at(1) == 0) return cudaSuccess;
+  const char* env = getenv("NB");
+  const int nb = env ? atoi(env) : units_at(2 * kUnit) >= many ? 2 : 1;
+  if (nb == 4)
+    return launch_norm_rope_t<D, 4>(p, interleaved, units_at(4 * kUnit), stream);
+  if (nb == 2)
+    return launch_norm_rope_t<D, 2>(p, interleaved, units_at(2 * kUnit), stream);
+  return launch_norm_rope_t<D, 1>(p, interleaved, units_at(kUnit), stream);
+}
+
+cudaError_t launch_norm_rope(const NormRopeParams& p, int D, bool interleaved, int num_sms,
                              cudaStream_t stream) {
-  return D == 64 ? launch_norm_rope_d<64>(p, interleaved, stream)
-                 : launch_norm_rope_d<128>(p, interleaved, stream);
+  return D == 64 ? launch_norm_rope_d<64>(p, interleaved, num_sms, stream)
+                 : launch_norm_rope_d<128>(p, interleaved, num_sms, stream);
 }
 
 cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, float* dqw,
                                  float* dkw, int num_sms, cudaStream_t stream) {
+  const int groups = kNrThreads / (D / 8);
   const long long uq = (p.q_heads + kBwdUnit - 1) / kBwdUnit;
   const long long uk = (p.kv_heads + kBwdUnit - 1) / kBwdUnit;
-  const int groups = kNrThreads / (D / 8);
   const long long needed = (p.total_tokens * (uq + uk) + groups - 1) / groups;
   // Three CTAs a SM, shared out by the number of heads; at least one for each.
   long long grid = num_sms * 3LL < kNormRopeBwdCtas ? num_sms * 3LL : kNormRopeBwdCtas;
@@ -431,14 +508,15 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, f
   p.q_ctas = static_cast<int>(gq);
   const unsigned g = static_cast<unsigned>(grid);
   if (p.total_tokens > 0) {
-    if (D == 64) {
-      if (interleaved) norm_rope_bwd_kernel<64, true><<<g, kNrThreads, 0, stream>>>(p);
-      else norm_rope_bwd_kernel<64, false><<<g, kNrThreads, 0, stream>>>(p);
-    } else {
-      if (interleaved) norm_rope_bwd_kernel<128, true><<<g, kNrThreads, 0, stream>>>(p);
-      else norm_rope_bwd_kernel<128, false><<<g, kNrThreads, 0, stream>>>(p);
-    }
-    const cudaError_t e = cudaGetLastError();
+    auto kern = D == 64 ? (interleaved ? norm_rope_bwd_kernel<64, true>
+                                       : norm_rope_bwd_kernel<64, false>)
+                        : (interleaved ? norm_rope_bwd_kernel<128, true>
+                                       : norm_rope_bwd_kernel<128, false>);
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<g, kNrThreads, kBwdSmem, stream>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (p.q_weight == nullptr) return cudaSuccess;

@@ -180,7 +180,8 @@ extern "C" int cpattn_qk_norm_rope(const void* q, int64_t q_stride, const void* 
   p.total_tokens = total_tokens;
   p.eps = eps;
   p.status = status;
-  return launch_norm_rope(p, head_dim, interleaved != 0, static_cast<cudaStream_t>(stream)) ==
+  return launch_norm_rope(p, head_dim, interleaved != 0, dev.num_sms,
+                          static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
@@ -332,7 +333,8 @@ extern "C" int cpattn_paged_append(
   p.page_shift = shift;
   p.max_pages = max_pages;
   p.page_stride = page_stride;
-  return launch_norm_rope(p, head_dim, interleaved != 0, static_cast<cudaStream_t>(stream)) ==
+  return launch_norm_rope(p, head_dim, interleaved != 0, dev.num_sms,
+                          static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
