@@ -255,12 +255,15 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, f
 // kernels run one CTA per (split, KV head).
 constexpr int kPagedMaxGroup = 128;
 
-// One split, written by the schedule kernel (two 16-byte loads).
+// One split, written by the schedule kernel (three 16-byte loads).
 struct alignas(16) PagedWork {
   int tok0, q_len, kv_len, seq;
   int blk;           // row block
   int kv_lo, kv_hi;  // keys [kv_lo, kv_hi), kv_lo a multiple of the unit
   int slot;          // slot of the partial results; -1: the item is whole
+  int slot0, n;      // a split item: its first slot and its splits
+  int item;          // a split item: its number among them
+  int pad;
 };
 
 // One item whose splits the merge kernel joins.
@@ -270,7 +273,7 @@ struct alignas(16) PagedMerge {
 };
 
 struct PagedLayout {
-  size_t first_off, work_off, merge_off, o_off, lse_off, total;
+  size_t first_off, work_off, merge_off, arrived_off, o_off, lse_off, total;
   int64_t max_work;   // splits of one KV head
   int64_t max_slots;  // slots of one KV head
 };
@@ -282,6 +285,7 @@ struct PagedShape {
   int unit;        // keys of a unit
   int min_units;   // an item is split only above this many units
   int ctas;        // a split does at least 1 / ctas of the whole work
+  bool join;       // the last CTA of a split item joins it (else a merge kernel)
 };
 
 struct PagedParams {
@@ -298,6 +302,7 @@ struct PagedParams {
   int* first;         // [num_seqs + 1]: first item of each sequence
   PagedWork* work;    // [max_work]
   PagedMerge* merge;  // [max_slots / 2]
+  int* arrived;       // [max_slots / 2, num_kv_heads]: splits that are done (register kernel)
   float* o_part;      // [max_slots, num_kv_heads, rows, D], normalised
   float* lse_part;    // [max_slots, num_kv_heads, rows], natural log
   long long max_work, max_slots;

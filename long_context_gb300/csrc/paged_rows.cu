@@ -31,6 +31,7 @@ constexpr int kPrWarps = kPrThreads / 32;
 constexpr int kGroupKeys = 16;
 constexpr float kNegInfR = -__builtin_huge_valf();
 constexpr float kLn2R = 0.69314718055994530942f;
+constexpr float kLog2eR = 1.44269504088896340736f;
 constexpr float kMoveBy = 8.0f;  // powers of two
 
 template <int D>
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   constexpr int kRpi = 32 / kCh;     // rows one warp copy covers
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kPrWarps][kRows], s_l[kPrWarps][kRows];
+  __shared__ int s_last;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   const int h = static_cast<int>(blockIdx.x) - e * Hk;
   if (e >= __ldcg(&p.hdr->n_items)) return;
   const int4* wp = reinterpret_cast<const int4*>(p.work + e);
-  const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1);
+  const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1), w2 = __ldcg(wp + 2);
   const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
   const int blk = w1.x, kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
   // Rows of this block: [row0, row0 + kRows), those below 0 are not there.
@@ -266,44 +268,140 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
             make_float2(o[mt][f][2 * hf], o[mt][f][2 * hf + 1]);
     }
   __syncthreads();
-  const float* all = reinterpret_cast<const float*>(smem);
-  for (int x = threadIdx.x; x < kRows * (D / 4); x += kPrThreads) {
-    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
-    const int row = row0 + r;
-    if (row < 0) continue;
-    float top = kNegInfR;
+  // Joins the warps' states: to the partial results of `to` (a slot), or to
+  // the output (to < 0).
+  auto join = [&](int to) {
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (int x = threadIdx.x; x < kRows * (D / 4); x += kPrThreads) {
+      const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+      const int row = row0 + r;
+      if (row < 0) continue;
+      float top = kNegInfR;
 #pragma unroll
-    for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, s_m[w][r]);
-    float den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, s_m[w][r]);
+      float den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kPrWarps; ++w) {
-      // A warp without a visible key has l = 0 and O = 0 (or NaN in both, which
-      // the row then shows).
-      const float f = s_m[w][r] == kNegInfR ? 1.f : ex2_approx(s_m[w][r] - top);
-      den = fmaf(f, s_l[w][r], den);
-      const float4 v = *reinterpret_cast<const float4*>(all + (w * kRows + r) * D + c);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+      for (int w = 0; w < kPrWarps; ++w) {
+        // A warp without a visible key has l = 0 and O = 0 (or NaN in both,
+        // which the row then shows).
+        const float f = s_m[w][r] == kNegInfR ? 1.f : ex2_approx(s_m[w][r] - top);
+        den = fmaf(f, s_l[w][r], den);
+        const float4 v = *reinterpret_cast<const float4*>(all + (w * kRows + r) * D + c);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      const float ref = top == kNegInfR ? 0.f : top;
+      const float lse = den == 0.f ? kNegInfR : (ref + __log2f(den)) * kLn2R;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (to >= 0) {
+        const size_t part = (static_cast<size_t>(to) * Hk + h) * kRows + r;
+        *reinterpret_cast<float4*>(p.o_part + part * D + c) = acc;
+        if (c == 0) p.lse_part[part] = lse;
+      } else {
+        const int tok = row / G;
+        const size_t at_row =
+            static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (row - tok * G);
+        *reinterpret_cast<uint2*>(p.out + at_row * D + c) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (c == 0 && p.lse != nullptr) p.lse[at_row] = lse;
+      }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    const float ref = top == kNegInfR ? 0.f : top;
-    const float lse = den == 0.f ? kNegInfR : (ref + __log2f(den)) * kLn2R;
-    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (slot >= 0) {
-      const size_t part = (static_cast<size_t>(slot) * Hk + h) * kRows + r;
-      *reinterpret_cast<float4*>(p.o_part + part * D + c) = acc;
-      if (c == 0) p.lse_part[part] = lse;
-    } else {
-      const int tok = row / G;
-      const size_t at_row = static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (row - tok * G);
-      *reinterpret_cast<uint2*>(p.out + at_row * D + c) =
-          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-      if (c == 0 && p.lse != nullptr) p.lse[at_row] = lse;
+  };
+  join(slot);
+  if (slot < 0 || MT > 1) return;  // 32 rows: see paged_merge_kernel
+
+  // The last of an item's splits to be done joins them all, in their order:
+  // each warp takes every fourth split, with its own running maximum.
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(p.arrived + static_cast<size_t>(w2.z) * Hk + h, 1) == w2.y - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
+  const int splits = w2.y;
+  const size_t part0 = (static_cast<size_t>(w2.x) * Hk + h) * kRows;
+  const size_t pitch = static_cast<size_t>(Hk) * kRows;  // rows from split to split
+  constexpr int kPer = D / 32;                          // floats of a row each lane owns
+  constexpr int kAhead = 4;                             // splits in flight of each of
+  constexpr int kAbreast = 4;                           // so many rows
+  for (int r0 = max(0, -row0); r0 < kRows; r0 += kAbreast) {
+    float mx[kAbreast], sum[kAbreast], acc[kAbreast][kPer];
+#pragma unroll
+    for (int i = 0; i < kAbreast; ++i) {
+      mx[i] = kNegInfR;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) acc[i][q] = 0.f;
+    }
+    for (int s0 = warp; s0 < splits; s0 += kAhead * kPrWarps) {
+      float x[kAbreast][kAhead], v[kAbreast][kAhead][kPer];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int s = s0 + u * kPrWarps;
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i) {
+          x[i][u] = kNegInfR;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) v[i][u][q] = 0.f;
+          if (s < splits && r0 + i < kRows) {
+            const size_t part = part0 + s * pitch + r0 + i;
+            x[i][u] = __ldcg(p.lse_part + part) * kLog2eR;
+            const float* src = p.o_part + part * D + lane * kPer;
+            if (kPer == 4) {
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+              v[i][u][0] = f.x;
+              v[i][u][1] = f.y;
+              v[i][u][2 % kPer] = f.z;
+              v[i][u][3 % kPer] = f.w;
+            } else {
+              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+              v[i][u][0] = f.x;
+              v[i][u][1] = f.y;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAbreast; ++i) {
+        float mn = mx[i];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) mn = fmaxf(mn, x[i][u]);
+        const float alpha = mx[i] == kNegInfR ? 0.f : ex2_approx(mx[i] - mn);
+        mx[i] = mn;
+        sum[i] *= alpha;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) acc[i][q] *= alpha;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const float f = x[i][u] == kNegInfR ? 0.f : ex2_approx(x[i][u] - mn);
+          sum[i] += f;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) acc[i][q] = fmaf(f, v[i][u][q], acc[i][q]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAbreast; ++i) {
+      const int r = r0 + i;
+      if (r >= kRows) break;
+      if (lane == 0) {
+        s_m[warp][r] = mx[i];
+        s_l[warp][r] = sum[i];
+      }
+#pragma unroll
+      for (int q = 0; q < kPer; q += 2)
+        *reinterpret_cast<float2*>(so + r * D + lane * kPer + q) =
+            make_float2(acc[i][q], acc[i][q + 1]);
     }
   }
+  __syncthreads();
+  join(-1);
 }
 
 template <int D, int MT>

@@ -59,6 +59,7 @@ PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
   PagedShape s;
   const int64_t rows = group * max_seqlen;
   s.tiles = rows > 32;
+  s.join = rows <= 16;
   if (s.tiles) {
     s.rows = kNQ * static_cast<int>(kBM / group * group);
     s.unit = kBN;
@@ -111,6 +112,8 @@ PagedLayout paged_layout(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int3
   off = serve_align(off + sizeof(PagedWork) * static_cast<size_t>(l.max_work));
   l.merge_off = off;
   off = serve_align(off + sizeof(PagedMerge) * static_cast<size_t>(l.max_slots / 2 + 1));
+  l.arrived_off = off;
+  off = serve_align(off + sizeof(int) * static_cast<size_t>(l.max_slots / 2 + 1) * Hk);
   const size_t rows = static_cast<size_t>(l.max_slots) * Hk * s.rows;
   l.o_off = off;
   off = serve_align(off + rows * D * sizeof(float));
@@ -423,6 +426,7 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   p.first = reinterpret_cast<int*>(ws + lay.first_off);
   p.work = reinterpret_cast<PagedWork*>(ws + lay.work_off);
   p.merge = reinterpret_cast<PagedMerge*>(ws + lay.merge_off);
+  p.arrived = reinterpret_cast<int*>(ws + lay.arrived_off);
   p.o_part = reinterpret_cast<float*>(ws + lay.o_off);
   p.lse_part = reinterpret_cast<float*>(ws + lay.lse_off);
   p.max_work = lay.max_work;
@@ -442,7 +446,7 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
     return CPATTN_ERR_CUDA;
   }
   // An item of no more than min_units units is never split.
-  if (max_kv_len > p.shape.min_units * p.shape.unit &&
+  if (!p.shape.join && max_kv_len > p.shape.min_units * p.shape.unit &&
       launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   return CPATTN_OK;
