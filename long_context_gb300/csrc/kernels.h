@@ -285,6 +285,7 @@ struct PagedShape {
   int unit;        // keys of a unit
   int min_units;   // an item is split only above this many units
   int ctas;        // a split does at least 1 / ctas of the whole work
+  int round;       // CTAs resident at once (at most ctas)
   bool join;       // the last CTA of a split item joins it (else a merge kernel)
 };
 

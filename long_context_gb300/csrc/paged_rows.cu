@@ -37,8 +37,9 @@ constexpr float kMoveBy = 8.0f;  // powers of two
 template <int D>
 struct RowsCfg {
   static constexpr int kHalf = kGroupKeys * D * 2;  // K (or V) of one group
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kGroups = D == 128 ? 1 : 2;  // groups of a step
+  static constexpr int kStage = kGroups * 2 * kHalf;
+  static constexpr int kStages = 3;
   static constexpr int kSmem = kPrWarps * kStages * kStage;  // 96 KB: two CTAs a SM
 };
 
@@ -82,38 +83,47 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   const size_t row_pitch = static_cast<size_t>(Hk) * D;
   const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
 
-  // Groups of this warp: kv_lo / 16 + warp, + 4, ...
+  // Groups of this warp: kv_lo / 16 + warp, + 4, ...; kGroups of them a step.
+  constexpr int NG = C::kGroups;
   const int n_groups = (kv_hi - kv_lo + kGroupKeys - 1) / kGroupKeys;
   const int n = n_groups > warp ? (n_groups - warp + kPrWarps - 1) / kPrWarps : 0;
+  const int steps = (n + NG - 1) / NG;
   auto group_key = [&](int j) { return kv_lo + (warp + j * kPrWarps) * kGroupKeys; };
-  int next_page = n > 0 ? __ldg(pages + (group_key(0) >> p.page_shift)) : 0;
-  auto copy = [&](int j) {
-    if (j < n) {
-      const int key0 = group_key(j);
-      int page = next_page;
-      if (j + 1 < n) next_page = __ldg(pages + (group_key(j + 1) >> p.page_shift));
-      int last = kv_len;  // keys at or beyond it are filled with zeros
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) atomicCAS(&p.hdr->error, 0, 1);  // CPATTN_ERR_INVALID_ARG
-        page = 0;
-        last = 0;
-      }
-      const int r0 = lane / kCh, c = lane % kCh;
-      const size_t off = static_cast<size_t>(page) * p.page_stride +
-                         static_cast<size_t>((key0 & page_mask) + r0) * row_pitch +
-                         static_cast<size_t>(h) * D + c * 8;
-      const __nv_bfloat16* ks = p.k_cache + off;
-      const __nv_bfloat16* vs = p.v_cache + off;
-      const uint32_t dst = ring + (j % C::kStages) * C::kStage;
+  int next_page[NG];
 #pragma unroll
-      for (int it = 0; it < kGroupKeys / kRpi; ++it) {
-        const int r = r0 + it * kRpi;
-        const bool in = key0 + r < last;
-        const size_t step = in ? it * kRpi * row_pitch : 0;
-        const __nv_bfloat16* kr = in ? ks + step : p.k_cache;
-        const __nv_bfloat16* vr = in ? vs + step : p.v_cache;
-        cp_async16(dst + at<D>(r, c), kr, in ? 16 : 0);
-        cp_async16(dst + C::kHalf + at<D>(r, c), vr, in ? 16 : 0);
+  for (int g = 0; g < NG; ++g)
+    next_page[g] = g < n ? __ldg(pages + (group_key(g) >> p.page_shift)) : 0;
+  auto copy = [&](int step) {
+    if (step < steps) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int j = step * NG + g;
+        const int key0 = group_key(j);
+        int page = next_page[g];
+        if (j + NG < n) next_page[g] = __ldg(pages + (group_key(j + NG) >> p.page_shift));
+        int last = j < n ? kv_len : 0;  // keys at or beyond it are filled with zeros
+        if (page < 0 || page >= p.num_pages) {
+          if (lane == 0 && j < n) atomicCAS(&p.hdr->error, 0, 1);  // CPATTN_ERR_INVALID_ARG
+          page = 0;
+          last = 0;
+        }
+        const int r0 = lane / kCh, c = lane % kCh;
+        const size_t off = static_cast<size_t>(page) * p.page_stride +
+                           static_cast<size_t>((key0 & page_mask) + r0) * row_pitch +
+                           static_cast<size_t>(h) * D + c * 8;
+        const __nv_bfloat16* ks = p.k_cache + off;
+        const __nv_bfloat16* vs = p.v_cache + off;
+        const uint32_t dst = ring + (step % C::kStages) * C::kStage + g * 2 * C::kHalf;
+#pragma unroll
+        for (int it = 0; it < kGroupKeys / kRpi; ++it) {
+          const int r = r0 + it * kRpi;
+          const bool in = key0 + r < last;
+          const size_t skip = in ? it * kRpi * row_pitch : 0;
+          const __nv_bfloat16* kr = in ? ks + skip : p.k_cache;
+          const __nv_bfloat16* vr = in ? vs + skip : p.v_cache;
+          cp_async16(dst + at<D>(r, c), kr, in ? 16 : 0);
+          cp_async16(dst + C::kHalf + at<D>(r, c), vr, in ? 16 : 0);
+        }
       }
     }
     cp_async_commit();
@@ -160,36 +170,48 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   }
 
 #pragma unroll 1
-  for (int j = 0; j < n; ++j) {
+  for (int step = 0; step < steps; ++step) {
     cp_async_wait<C::kStages - 2>();
     __syncwarp();
-    copy(j + C::kStages - 1);
-    const uint32_t kb = ring + (j % C::kStages) * C::kStage;
+    copy(step + C::kStages - 1);
+    const uint32_t kb = ring + (step % C::kStages) * C::kStage;
     const uint32_t vb = kb + C::kHalf;
-    float s[MT][2][4];
+    float s[NG][MT][2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t b[4];
-      ldmatrix4(kb + at<D>((lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), b);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma_16816(s[mt][0], qa[mt][kk], b[0], b[1]);
-        mma_16816(s[mt][1], qa[mt][kk], b[2], b[3]);
-      }
-    }
-    const int key0 = group_key(j);
-    if (key0 + kGroupKeys > free_end) {
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int key = key0 + (i >> 2) * 8 + 2 * (lane & 3) + (i & 1);
-          if (key >= lim[mt][(i >> 1) & 1]) s[mt][i >> 2][i & 3] = kNegInfR;
+        for (int i = 0; i < 8; ++i) s[g][mt][i >> 2][i & 3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t b[4];
+        ldmatrix4(kb + g * 2 * C::kHalf +
+                      at<D>((lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)),
+                  b);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_16816(s[g][mt][0], qa[mt][kk], b[0], b[1]);
+          mma_16816(s[g][mt][1], qa[mt][kk], b[2], b[3]);
         }
+      }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      // A step's groups beyond the last hold zeros and lie beyond every limit
+      // (or beyond kv_hi, which a following split starts with: masked too).
+      const int j = step * NG + g;
+      const int key0 = group_key(j);
+      if (key0 + kGroupKeys > free_end || j >= n) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = key0 + (i >> 2) * 8 + 2 * (lane & 3) + (i & 1);
+            if (key >= lim[mt][(i >> 1) & 1] || j >= n) s[g][mt][i >> 2][i & 3] = kNegInfR;
+          }
+      }
     }
     bool move = false;
     float top[MT][2];
@@ -197,8 +219,11 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float t = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
-                        fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+        float t = kNegInfR;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          t = fmaxf(t, fmaxf(fmaxf(s[g][mt][0][2 * hf], s[g][mt][0][2 * hf + 1]),
+                             fmaxf(s[g][mt][1][2 * hf], s[g][mt][1][2 * hf + 1])));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
         top[mt][hf] = t * p.scale_log2;
@@ -220,28 +245,33 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
           }
         }
     }
-    uint32_t pa[MT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int g = 0; g < NG; ++g) {
+      uint32_t pa[MT][4];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float ref = m[mt][hf] == kNegInfR ? 0.f : m[mt][hf];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2_approx(fmaf(s[mt][t][2 * hf], p.scale_log2, -ref));
-          const float p1 = ex2_approx(fmaf(s[mt][t][2 * hf + 1], p.scale_log2, -ref));
-          l[mt][hf] += p0 + p1;
-          pa[mt][2 * t + hf] = pack_bf16x2(p0, p1);
+        for (int hf = 0; hf < 2; ++hf) {
+          const float ref = m[mt][hf] == kNegInfR ? 0.f : m[mt][hf];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float p0 = ex2_approx(fmaf(s[g][mt][t][2 * hf], p.scale_log2, -ref));
+            const float p1 = ex2_approx(fmaf(s[g][mt][t][2 * hf + 1], p.scale_log2, -ref));
+            l[mt][hf] += p0 + p1;
+            pa[mt][2 * t + hf] = pack_bf16x2(p0, p1);
+          }
         }
-      }
 #pragma unroll
-    for (int f = 0; f < D / 16; ++f) {
-      uint32_t b[4];
-      ldmatrix4_trans(vb + at<D>((lane & 7) + (((lane >> 3) & 1) << 3), f * 2 + (lane >> 4)), b);
+      for (int f = 0; f < D / 16; ++f) {
+        uint32_t b[4];
+        ldmatrix4_trans(vb + g * 2 * C::kHalf +
+                            at<D>((lane & 7) + (((lane >> 3) & 1) << 3), f * 2 + (lane >> 4)),
+                        b);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma_16816(o[mt][2 * f], pa[mt], b[0], b[1]);
-        mma_16816(o[mt][2 * f + 1], pa[mt], b[2], b[3]);
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_16816(o[mt][2 * f], pa[mt], b[0], b[1]);
+          mma_16816(o[mt][2 * f + 1], pa[mt], b[2], b[3]);
+        }
       }
     }
   }

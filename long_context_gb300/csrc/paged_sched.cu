@@ -139,7 +139,12 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   }
   ps_scan<NT>(sum, warp_sums);
   const long long all = warp_sums[NT / 32 - 1];
-  long long target = (all * p.num_kv_heads + p.shape.ctas - 1) / p.shape.ctas;
+  // With few items the splits are made to fit one round of resident CTAs
+  // (sum of ceil(u / target) <= all / target + items), else to be several
+  // rounds that even out.
+  const long long lanes = static_cast<long long>(items) * p.num_kv_heads;
+  const long long share = 2 * lanes <= p.shape.round ? p.shape.round - lanes : p.shape.ctas;
+  long long target = (all * p.num_kv_heads + share - 1) / share;
   if (target < p.shape.min_units) target = p.shape.min_units;
   __syncthreads();
 

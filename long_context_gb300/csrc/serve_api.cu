@@ -65,11 +65,13 @@ PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
     s.unit = kBN;
     s.min_units = 8;
     s.ctas = 304;
+    s.round = 152;
   } else {
     s.rows = rows <= 16 ? 16 : 32;
     s.unit = 64;
     s.min_units = 1;
     s.ctas = 608;
+    s.round = 304;
   }
   return s;
 }
