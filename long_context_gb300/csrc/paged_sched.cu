@@ -1,13 +1,27 @@
 // Attention over a paged KV cache: the work list, and the merge of splits.
 //
 // The schedule kernel reads the lengths on the device (a captured graph can be
-// replayed with other lengths) and cuts the work: with W units of keys over
-// all items of a KV head, an item of u units becomes ceil(u / target) splits,
-//   target = max(min_units, ceil(W * KV heads / ctas)),
-// so every CTA has at most 1 / ctas of the work and a long cache with few new
-// tokens still fills the GPU.  Since an item of more than one split has more
-// than target units, split items have at most 2 W / target <= 2 ctas / heads
-// splits in all, which bounds the partial results' memory on the host.
+// replayed with other lengths) and cuts the work.  W is the units of keys over
+// all items of one KV head; every KV head is cut alike.
+//
+// Few rows (HBM bound; two CTAs a SM): an item of u units becomes
+// ceil(u / target) equal splits, target = max(min_units, ceil(W heads / ctas)).
+//
+// Tiles (one CTA a SM, an item is up to hundreds of units): the items' units are
+// laid end to end and cut at every multiple of one SM's share
+// C = max(min_units, ceil(W heads / SMs)), unless the cut would fall within C / 16
+// of an item's end or the item has at most min_units (or, when an eighth of the
+// work is in items of less than C / 4, at most C).  So items that divide badly among the SMs are evened out by
+// at most one cut a SM, and the splits are listed by decreasing size, which the
+// hardware then starts in that order as SMs become free.  (2,048 tokens over
+// 32,768, 256 items of 272 units on 152 SMs: 814 us with each item halved,
+// two rounds of whole items 816 us; cut this way 741 us.)
+//
+// Either way the split items have at most 2 ctas / heads splits in all (an item
+// of n > 1 splits has more than (n - 1) target units, or n - 1 cuts), which
+// bounds the partial results' memory on the host.  Which items are cut, and
+// where, depends on the lengths alone; only the order of equally large splits
+// in the list is left to chance, and no result depends on it.
 //
 // The merge joins an item's normalised partials: LSE = ln sum exp(lse_s),
 // O = sum exp(lse_s - LSE) O_s.
@@ -19,6 +33,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kPmThreads = 256;
+constexpr int kBuckets = 128;  // sizes told apart in the list's order (at most NT)
 constexpr float kNegInfP = -__builtin_huge_valf();
 
 // Inclusive scan over the block; warp_sums[NT / 32 - 1] holds the total after it.
@@ -88,9 +103,11 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   __shared__ long long warp_sums[32];
   __shared__ int s_bad;
   __shared__ int s_first[kPsThreads + 1];  // first item of each sequence (small batches)
-  __shared__ int s_base[kPsThreads];       // first split of each item of a round
+  __shared__ int s_base[kPsThreads + 1];   // first split of each item of a round
+  __shared__ int s_bucket[kBuckets];       // splits by size
+  __shared__ long long s_round;
   __shared__ PagedItem s_item[kPsThreads];
-  __shared__ int2 s_split[kPsThreads];     // units of a split, first slot (-1: whole)
+  __shared__ int2 s_split[kPsThreads];     // units of the first split, first slot (-1: whole)
   __shared__ int s_number[kPsThreads];     // number among the split items
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
@@ -131,6 +148,7 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   }
 
   // All units, and the largest split that shares them out.
+  const bool tiles = p.shape.tiles;
   long long sum = 0;
   PagedItem it = {};
   for (int i = tid; i < items; i += kPsThreads) {
@@ -139,73 +157,145 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   }
   ps_scan<NT>(sum, warp_sums);
   const long long all = warp_sums[NT / 32 - 1];
-  // With few items the splits are made to fit one round of resident CTAs
+  // Few rows, few items: the splits are made to fit one round of resident CTAs
   // (sum of ceil(u / target) <= all / target + items), else to be several
   // rounds that even out.
   const long long lanes = static_cast<long long>(items) * p.num_kv_heads;
-  const long long share = 2 * lanes <= p.shape.round ? p.shape.round - lanes : p.shape.ctas;
-  long long target = (all * p.num_kv_heads + share - 1) / share;
-  if (target < p.shape.min_units) target = p.shape.min_units;
+  const long long share =
+      !tiles && 2 * lanes <= p.shape.round ? p.shape.round - lanes : p.shape.ctas;
+  long long target_ll = (all * p.num_kv_heads + share - 1) / share;
+  if (target_ll < p.shape.min_units) target_ll = p.shape.min_units;
+  const int target = static_cast<int>(min(target_ll, 1ll << 30));
+  const int snap = target / 16 + 1;
+  // Tiles: when small items hold an eighth of the work, they even out the SMs
+  // by themselves (started last), and only items above a share are cut.
+  int uncut = p.shape.min_units;  // items of at most so many units stay whole
+  if (tiles) {
+    long long small_sum = 0;
+    __syncthreads();
+    for (int i = tid; i < items; i += kPsThreads) {
+      if (!(items <= kPsThreads)) it = paged_item(p, first, i);
+      const int units = item_units(p, it);
+      if (units <= target / 4) small_sum += units;
+    }
+    ps_scan<NT>(small_sum, warp_sums);
+    if (warp_sums[NT / 32 - 1] * 8 >= all) uncut = target > uncut ? target : uncut;
+  }
+  for (int i = tid; i < kBuckets; i += kPsThreads) s_bucket[i] = 0;
   __syncthreads();
 
+  // Pass 0 (tiles) counts the splits of each size, pass 1 writes the list.
+  const bool once = items <= kPsThreads;
   int work0 = 0, slot0 = 0, merge0 = 0;
-  for (int base = 0; base < items; base += kPsThreads) {
-    const int i = base + tid;
-    int n = 0, per = 0;
-    if (i < items) {
-      if (items > kPsThreads) it = paged_item(p, first, i);
-      const int units = item_units(p, it);
-      n = units > target ? static_cast<int>((units + target - 1) / target) : 1;
-      per = (units + n - 1) / n;
-      if (n > 1) n = (units + per - 1) / per;
+  for (int pass = tiles ? 0 : 1; pass < 2; ++pass) {
+    work0 = slot0 = merge0 = 0;
+    long long unit0 = 0;
+    for (int base = 0; base < items; base += kPsThreads) {
+      const int in_round = min(items - base, kPsThreads);
+      long long round;
+      if (pass == 0 || !tiles || !once) {
+        const int i = base + tid;
+        int n = 0, cut = 0, units = 0;
+        if (i < items) {
+          if (!once) it = paged_item(p, first, i);
+          units = item_units(p, it);
+        }
+        if (tiles) {
+          // The item is [at, at + units) of the units laid end to end.
+          const long long at = unit0 + ps_scan<NT>(units, warp_sums) - units;
+          unit0 += warp_sums[NT / 32 - 1];
+          __syncthreads();
+          if (i < items) {
+            const long long m0 = (at + snap) / target + 1;
+            const long long m1 = (at + units - snap - 1) / target;
+            n = units > uncut && m1 >= m0 ? static_cast<int>(m1 - m0) + 2 : 1;
+            cut = n > 1 ? static_cast<int>(m0 * target - at) : units;
+          }
+        } else if (i < items) {
+          n = units > target ? (units + target - 1) / target : 1;
+          cut = (units + n - 1) / n;
+          if (n > 1) n = (units + cut - 1) / cut;
+        }
+        const bool split = n > 1;
+        // Splits, slots and merges counted in one scan (slots and merges < 2^16).
+        const long long v = n + (split ? (static_cast<long long>(n) << 32) + (1ll << 48) : 0);
+        const long long before = ps_scan<NT>(v, warp_sums) - v;
+        round = warp_sums[NT / 32 - 1];
+        const int slot = slot0 + static_cast<int>((before >> 32) & 0xffff);
+        const int item = merge0 + static_cast<int>(before >> 48);
+        s_base[tid] = static_cast<int>(before & 0xffffffffll);
+        s_item[tid] = it;
+        s_split[tid] = make_int2(cut, split ? slot : -1);
+        s_number[tid] = item;
+        if (pass == 1 && split && !p.shape.join) {
+          PagedMerge m = {};
+          m.tok0 = it.tok0;
+          m.q_len = it.q_len;
+          m.blk = it.blk;
+          m.slot0 = slot;
+          m.n = n;
+          p.merge[item] = m;
+        }
+        if (tid == 0) s_base[kPsThreads] = static_cast<int>(round & 0xffffffffll);
+        __syncthreads();
+        if (tid == 0) s_round = round;
+      } else {
+        // One round: still there from pass 0, but for the merges.
+        round = s_round;
+        if (tid < in_round && s_split[tid].y >= 0 && !p.shape.join) {
+          PagedMerge m = {};
+          m.tok0 = it.tok0;
+          m.q_len = it.q_len;
+          m.blk = it.blk;
+          m.slot0 = s_split[tid].y;
+          m.n = (tid + 1 < in_round ? s_base[tid + 1] : s_base[kPsThreads]) - s_base[tid];
+          p.merge[s_number[tid]] = m;
+        }
+      }
+      const int splits = static_cast<int>(round & 0xffffffffll);
+      for (int e = tid; e < splits; e += kPsThreads) {
+        const int x = last_le(s_base, in_round, e);
+        const PagedItem t = s_item[x];
+        const int2 sp = s_split[x];
+        const int n = (x + 1 < in_round ? s_base[x + 1] : splits) - s_base[x];
+        const int s = e - s_base[x];
+        const int step = tiles ? target : sp.x;
+        const int units = item_units(p, t);
+        const int u0 = s == 0 ? 0 : sp.x + (s - 1) * step;
+        const int u1 = s == n - 1 ? units : sp.x + s * step;
+        const int bucket =
+            min(kBuckets - 1, static_cast<int>((u1 - u0) * static_cast<long long>(kBuckets) /
+                                               (target + 2 * snap)));
+        if (pass == 0) {
+          atomicAdd(&s_bucket[kBuckets - 1 - bucket], 1);
+          continue;
+        }
+        PagedWork w;
+        w.tok0 = t.tok0;
+        w.q_len = t.q_len;
+        w.kv_len = t.kv_len;
+        w.seq = t.seq;
+        w.blk = t.blk;
+        w.kv_lo = u0 * p.shape.unit;
+        w.kv_hi = s == n - 1 ? t.hi : u1 * p.shape.unit;
+        w.slot = sp.y < 0 ? -1 : sp.y + s;
+        w.slot0 = sp.y;
+        w.n = n;
+        w.item = s_number[x];
+        w.pad = 0;
+        p.work[tiles ? atomicAdd(&s_bucket[kBuckets - 1 - bucket], 1) : work0 + e] = w;
+      }
+      work0 += splits;
+      slot0 += static_cast<int>((round >> 32) & 0xffff);
+      merge0 += static_cast<int>(round >> 48);
+      __syncthreads();
     }
-    const bool split = n > 1;
-    // Splits, slots and merges counted in one scan (slots and merges < 2^16).
-    const long long v = n + (split ? (static_cast<long long>(n) << 32) + (1ll << 48) : 0);
-    const long long before = ps_scan<NT>(v, warp_sums) - v;
-    const long long round = warp_sums[NT / 32 - 1];
-    const int slot = slot0 + static_cast<int>((before >> 32) & 0xffff);
-    s_base[tid] = static_cast<int>(before & 0xffffffffll);
-    s_item[tid] = it;
-    const int item = merge0 + static_cast<int>(before >> 48);
-    s_split[tid] = make_int2(per, split ? slot : -1);
-    s_number[tid] = item;
-    if (split && !p.shape.join) {
-      PagedMerge m = {};
-      m.tok0 = it.tok0;
-      m.q_len = it.q_len;
-      m.blk = it.blk;
-      m.slot0 = slot;
-      m.n = n;
-      p.merge[item] = m;
+    if (pass == 0) {  // sizes in decreasing order: where each begins in the list
+      const int v = tid < kBuckets ? s_bucket[tid] : 0;
+      const int at = static_cast<int>(ps_scan<NT>(v, warp_sums)) - v;
+      if (tid < kBuckets) s_bucket[tid] = at;
+      __syncthreads();
     }
-    __syncthreads();
-    const int in_round = min(items - base, kPsThreads);
-    const int splits = static_cast<int>(round & 0xffffffffll);
-    for (int e = tid; e < splits; e += kPsThreads) {
-      const int x = last_le(s_base, in_round, e);
-      const PagedItem t = s_item[x];
-      const int2 sp = s_split[x];
-      const int s = e - s_base[x];
-      PagedWork w;
-      w.tok0 = t.tok0;
-      w.q_len = t.q_len;
-      w.kv_len = t.kv_len;
-      w.seq = t.seq;
-      w.blk = t.blk;
-      w.kv_lo = s * sp.x * p.shape.unit;
-      w.kv_hi = min(t.hi, (s + 1) * sp.x * p.shape.unit);
-      w.slot = sp.y < 0 ? -1 : sp.y + s;
-      w.slot0 = sp.y;
-      w.n = sp.y < 0 ? 1 : (item_units(p, t) + sp.x - 1) / sp.x;
-      w.item = s_number[x];
-      w.pad = 0;
-      p.work[work0 + e] = w;
-    }
-    work0 += splits;
-    slot0 += static_cast<int>((round >> 32) & 0xffff);
-    merge0 += static_cast<int>(round >> 48);
-    __syncthreads();
   }
   if (p.shape.join)
     for (int i = tid; i < merge0 * p.num_kv_heads; i += kPsThreads) p.arrived[i] = 0;

@@ -64,7 +64,7 @@ PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
     s.rows = kNQ * static_cast<int>(kBM / group * group);
     s.unit = kBN;
     s.min_units = 8;
-    s.ctas = 304;
+    s.ctas = 152;
     s.round = 152;
   } else {
     s.rows = rows <= 16 ? 16 : 32;
