@@ -1,7 +1,9 @@
 """Build step for the native library ``libcpattn.so`` (sm_103a).
 
 Compiles the CUDA/C++ sources under ``csrc/`` in parallel with nvcc and links
-them into ``long_context_gb300/libcpattn.so``.  The CUDA runtime is linked
+them into ``long_context_gb300/libcpattn.so``, and ``csrc/binding.cpp`` with the
+host compiler into the CPython module ``_binding.so`` beside it (against the
+installed PyTorch's headers).  The CUDA runtime is linked
 statically and the driver is reached through the runtime's entry-point query,
 so the library loads on a machine without a GPU (the host-only planner can run
 there) and needs only the NVIDIA driver on a GPU machine.
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcpattn.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 SOURCES = ["plan.cpp", "api.cu", "schedule.cu", "merge.cu", "attn_fwd.cu", "attn_bwd.cu",
            "dcp.cu", "decode.cu", "noalloc.cu", "ulysses.cu", "norm_rope.cu", "paged_sched.cu",
@@ -99,11 +104,55 @@ def build_debug(force=False):
     return _build_variant("cpattn_debug", "CPATTN_DEBUG", force)
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, r.stdout, r.stderr))
+
+
+def _torch_dir():
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_binding():
+    root = _torch_dir()
+    obj = os.path.join(BUILD, "binding.cpp.o")
+    inc = [os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(
+               os.path.realpath(_nvcc()))), "include"), INCLUDE]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SRC, "-o", obj]
+         + [x for p in inc for x in ("-isystem" if p != INCLUDE else "-I", p)], "g++ binding.cpp")
+    return obj
+
+
+def _link_binding(obj):
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libcpattn.so", "-Wl,-rpath,$ORIGIN",
+          "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+          "-ltorch", "-lc10_cuda", "-lc10"], "linking _binding.so")
+    os.replace(tmp, BINDING)
+
+
+def _binding_stale():
+    if not os.path.exists(BINDING):
+        return True
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "cpattn.h"), os.path.abspath(__file__),
+            os.path.join(_torch_dir(), "version.py")]
+    return any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps)
+
+
 def build(force=False, verbose_ptxas=False, quiet=True):
-    """Compile and link ``libcpattn.so`` unless it is up to date."""
-    if not force and not _stale():
-        return LIB
+    """Compile and link ``libcpattn.so`` and ``_binding.so`` unless they are up
+    to date."""
     os.makedirs(BUILD, exist_ok=True)
+    binding = force or _binding_stale()
+    if not force and not _stale():
+        if binding:
+            _link_binding(_compile_binding())
+        return LIB
     nvcc = _nvcc()
     flags = _flags(verbose_ptxas)
 
@@ -115,8 +164,10 @@ def build(force=False, verbose_ptxas=False, quiet=True):
             raise RuntimeError("nvcc failed on %s:\n%s\n%s" % (src, r.stdout, r.stderr))
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        obj = ex.submit(_compile_binding) if binding else None
         results = list(ex.map(compile_one, SOURCES))
+        obj = obj and obj.result()
     if not quiet or verbose_ptxas:
         for _, log in results:
             if log.strip():
@@ -128,6 +179,8 @@ def build(force=False, verbose_ptxas=False, quiet=True):
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    if binding:
+        _link_binding(obj)
     return LIB
 
 

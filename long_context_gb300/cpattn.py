@@ -4,7 +4,8 @@ Argument marshalling only: tensors are checked for dtype, device, layout and
 contiguity, then their device pointers are handed to ``libcpattn.so`` together
 with PyTorch's current CUDA stream.  Every step of the computation runs in the
 library's kernels; there is no fallback.  Importing this module raises
-``ImportError`` when the library has not been built (``build.build()``).
+``ImportError`` when the library (or the compiled part of this binding,
+``_binding.so``) has not been built (``build.build()``).
 """
 
 from __future__ import annotations
@@ -23,6 +24,11 @@ if not os.path.exists(_LIB_PATH):
         "libcpattn.so is missing at %s; build it with "
         "long_context_gb300.build.build()" % _LIB_PATH)
 _lib = ctypes.CDLL(_LIB_PATH)
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError("_binding.so is missing or does not match this PyTorch; build it with "
+                      "long_context_gb300.build.build()") from e
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -116,6 +122,9 @@ class CpattnError(RuntimeError):
     def __init__(self, status, what):
         self.status = status
         super().__init__("%s: %s (status %d)" % (what, status_string(status), status))
+
+
+_binding.set_error(CpattnError)
 
 
 # ---------------------------------------------------------------- tracing --
@@ -731,102 +740,7 @@ def merge(o_steps, m_steps, l_steps, *, out_o=None, out_m=None, out_l=None, stre
 
 # ------------------------------------------------- norm + rotation, paged cache --
 # These calls run once per layer of a decoding step, where the host's time
-# counts: every argument is first held against all its conditions at once, and
-# only a failed one is taken apart for its message.
-
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream
-
-
-def _run_on(dev, stream, made, fn, name, *args):
-    """Call ``fn(*args, stream)`` on the tensors' device and on ``stream`` (the
-    device's current stream when None).  ``made`` are the tensors this call
-    allocated: on a stream that is not current, the allocator has to be told
-    who uses them."""
-    index = dev.index
-    if stream is None:
-        handle = _raw_stream(index)
-    else:
-        if stream.device != dev:
-            raise ValueError("stream must be on %s, got %s" % (dev, stream.device))
-        handle = stream.cuda_stream
-        if handle != _raw_stream(index):
-            for t in made:
-                t.record_stream(stream)
-    if torch.cuda.current_device() == index:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, handle)
-    if st:
-        raise CpattnError(st, name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _shape_of(t, name, dims, form):
-    """The shape of a bf16 tensor of ``dims`` dimensions on a CUDA device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype is not _BF16:
-        raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
-    if t.dim() != dims:
-        raise ValueError("%s must be %s" % (name, form))
-    if not t.is_cuda:
-        raise ValueError("%s must be on a CUDA device, got %s" % (name, t.device))
-    return t.shape
-
-
-def _need_rows(t, name, dev, shape):
-    """A bf16 ``[T, heads, D]`` tensor whose tokens' heads are contiguous;
-    returns the elements from token to token."""
-    n, heads, d = shape
-    if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.device == dev
-            and t.shape == (n, heads, d)):
-        st, sh, sd = t.stride()
-        if sd == 1 and (sh == d or heads == 1):
-            return st if n > 1 else heads * d
-        if n * heads * d == 0:
-            return heads * d
-        raise ValueError("%s: the heads of a token must be contiguous" % name)
-    _shape_of(t, name, 3, "[T, heads, D]")
-    if t.device != dev:
-        raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
-    raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-
-
-def _need_flat(t, name, dtype, dev, shape):
-    """A contiguous tensor of that type, device and shape; returns its address."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _need(t, name, dtype, dev, shape)
-
-
-def _need_turn(positions, rope_table, q_weight, k_weight, T, D, dev):
-    """What the norm + rotation calls share: the addresses of the positions, the
-    table and the weights, the rotary dim and the positions in the table."""
-    pos = table = wq = wk = None
-    rot = max_pos = 0
-    if rope_table is not None:
-        if not isinstance(rope_table, torch.Tensor) or rope_table.dim() != 2:
-            raise ValueError("rope_table must be a [max_position, rotary_dim] tensor")
-        max_pos, rot = rope_table.shape
-        table = _need_flat(rope_table, "rope_table", _F32, dev, (max_pos, rot))
-        if T is not None:
-            pos = _need_flat(positions, "positions", _I32, dev, (T,))
-    if q_weight is not None:
-        wq = _need_flat(q_weight, "q_weight", _BF16, dev, (D,))
-    if k_weight is not None:
-        wk = _need_flat(k_weight, "k_weight", _BF16, dev, (D,))
-    return pos, table, rot, max_pos, wq, wk
-
-
-def _need_status(status, dev):
-    return None if status is None else _need_flat(status, "status", _I32, dev, (1,))
-
+# counts: ``_binding`` (csrc/binding.cpp) checks and marshals their arguments.
 
 @_traced("cpattn_qk_norm_rope")
 def qk_norm_rope(q, k, positions, rope_table, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -842,30 +756,8 @@ def qk_norm_rope(q, k, positions, rope_table, *, q_weight=None, k_weight=None, e
     may be ``q`` and ``k_out`` may be ``k``.  ``status``: int32 ``[1]``, set
     when a position is outside the table (its rows are left as they were).
     """
-    T, H, D = _shape_of(q, "q", 3, "[T, heads, D]")
-    dev = q.device
-    Hk = _shape_of(k, "k", 3, "[T, heads, D]")[1]
-    qs = _need_rows(q, "q", dev, (T, H, D))
-    ks = _need_rows(k, "k", dev, (T, Hk, D))
-    pos, table, rot, max_pos, wq, wk = _need_turn(positions, rope_table, q_weight, k_weight, T, D,
-                                                  dev)
-    made = []
-    if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=_BF16, device=dev)
-        qos = H * D
-        made.append(q_out)
-    else:
-        qos = _need_rows(q_out, "q_out", dev, (T, H, D))
-    if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=_BF16, device=dev)
-        kos = Hk * D
-        made.append(k_out)
-    else:
-        kos = _need_rows(k_out, "k_out", dev, (T, Hk, D))
-    _run_on(dev, stream, made, _lib.cpattn_qk_norm_rope, "cpattn_qk_norm_rope", q.data_ptr(), qs,
-            k.data_ptr(), ks, pos, table, rot, max_pos, wq, wk, eps, 1 if interleaved else 0, T, H,
-            Hk, D, q_out.data_ptr(), qos, k_out.data_ptr(), kos, _need_status(status, dev))
-    return q_out, k_out
+    return _binding.qk_norm_rope(q, k, positions, rope_table, q_weight, k_weight, eps, interleaved,
+                                 q_out, k_out, status, stream)
 
 
 @_traced("cpattn_qk_norm_rope_bwd")
@@ -879,86 +771,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, rope_table, *, q_weight=No
     ``dq_out``, ``dk_out``: the gradients of its outputs (token strides as the
     inputs'); the other arguments as in the call being differentiated.
     """
-    T, H, D = _shape_of(dq_out, "dq_out", 3, "[T, heads, D]")
-    dev = dq_out.device
-    Hk = _shape_of(dk_out, "dk_out", 3, "[T, heads, D]")[1]
-    gqs = _need_rows(dq_out, "dq_out", dev, (T, H, D))
-    gks = _need_rows(dk_out, "dk_out", dev, (T, Hk, D))
-    pos, table, rot, max_pos, wq, wk = _need_turn(positions, rope_table, q_weight, k_weight, T, D,
-                                                  dev)
-    normed = q_weight is not None or k_weight is not None
-    made = []
-
-    def new(shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(t)
-        return t
-
-    if dq is None:
-        dq, dqs = new((T, H, D), _BF16), H * D
-    else:
-        dqs = _need_rows(dq, "dq", dev, (T, H, D))
-    if dk is None:
-        dk, dks = new((T, Hk, D), _BF16), Hk * D
-    else:
-        dks = _need_rows(dk, "dk", dev, (T, Hk, D))
-    q_at = k_at = ws = dwq = dwk = None
-    qs = ks = ws_bytes = 0
-    if normed:
-        qs, ks = _need_rows(q, "q", dev, (T, H, D)), _need_rows(k, "k", dev, (T, Hk, D))
-        q_at, k_at = q.data_ptr(), k.data_ptr()
-        if dq_weight is None:
-            dq_weight = new(D, _F32)
-        if dk_weight is None:
-            dk_weight = new(D, _F32)
-        dwq = _need_flat(dq_weight, "dq_weight", _F32, dev, (D,))
-        dwk = _need_flat(dk_weight, "dk_weight", _F32, dev, (D,))
-        if workspace is None:
-            workspace = new(_lib.cpattn_qk_norm_rope_bwd_workspace_size(D), torch.uint8)
-        ws_bytes = workspace.numel()
-        ws = _need_flat(workspace, "workspace", torch.uint8, dev, (ws_bytes,))
-    elif dq_weight is not None or dk_weight is not None:
-        raise ValueError("dq_weight and dk_weight need q_weight and k_weight")
-    _run_on(dev, stream, made, _lib.cpattn_qk_norm_rope_bwd, "cpattn_qk_norm_rope_bwd",
-            dq_out.data_ptr(), gqs, dk_out.data_ptr(), gks, q_at, qs, k_at, ks, pos, table, rot,
-            max_pos, wq, wk, eps, 1 if interleaved else 0, T, H, Hk, D, dq.data_ptr(), dqs,
-            dk.data_ptr(), dks, dwq, dwk, ws, ws_bytes, _need_status(status, dev))
-    return dq, dk, dq_weight, dk_weight
-
-
-def _need_cache(k_cache, v_cache, page_table, cu_seqlens, kv_lens, dev, heads, D):
-    """A paged cache and its lengths: (pages, page size, elements from page to
-    page, sequences, pages of a table row, addresses of table, cu_seqlens,
-    kv_lens)."""
-    pages, size = _shape_of(k_cache, "k_cache", 4, "[num_pages, page_size, heads, D]")[:2]
-    shape = (pages, size, heads, D)
-    strides = []
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
-        if t.dtype is not _BF16:
-            raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
-        if t.device != dev:
-            raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
-        if t.shape != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-        if t.is_contiguous():
-            strides.append(size * heads * D)
-        else:
-            if pages > 0 and not t[0].is_contiguous():
-                raise ValueError("%s: a page must be contiguous" % name)
-            strides.append(t.stride(0))
-    if strides[0] != strides[1]:
-        raise ValueError("k_cache and v_cache must have the same page stride")
-    if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1:
-        raise ValueError("kv_lens must be a [num_seqs] tensor")
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be a [num_seqs, max_pages] tensor")
-    B, row = kv_lens.shape[0], page_table.shape[1]
-    return (pages, size, strides[0], B, row,
-            _need_flat(page_table, "page_table", _I32, dev, (B, row)),
-            _need_flat(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)),
-            _need_flat(kv_lens, "kv_lens", _I32, dev, (B,)))
+    return _binding.qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, rope_table, q_weight, k_weight,
+                                     eps, interleaved, dq, dk, dq_weight, dk_weight, workspace,
+                                     status, stream)
 
 
 @_traced("cpattn_paged_append")
@@ -975,33 +790,10 @@ def paged_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, rop
     ``[num_pages, page_size, Hk, D]``; ``page_table [B, max_pages]``: int32.
     ``status``: int32 ``[1]``, set when a token could not be placed.
     """
-    T, Hk, D = _shape_of(k, "k", 3, "[T, heads, D]")
-    dev = k.device
-    ks, vs = _need_rows(k, "k", dev, (T, Hk, D)), _need_rows(v, "v", dev, (T, Hk, D))
-    pages, size, page_stride, B, row, table_at, cu_at, kv_at = _need_cache(
-        k_cache, v_cache, page_table, cu_seqlens, kv_lens, dev, Hk, D)
-    _, rope, rot, max_pos, wq, wk = _need_turn(None, rope_table, q_weight, k_weight, None, D, dev)
-    made = []
-    H = qs = qos = 0
-    if q is not None:
-        H = _shape_of(q, "q", 3, "[T, heads, D]")[1]
-        qs = _need_rows(q, "q", dev, (T, H, D))
-        if q_out is None:
-            q_out = torch.empty((T, H, D), dtype=_BF16, device=dev)
-            qos = H * D
-            made.append(q_out)
-        else:
-            qos = _need_rows(q_out, "q_out", dev, (T, H, D))
-    elif q_out is not None or q_weight is not None:
-        raise ValueError("q_out and q_weight need q")
-    _run_on(dev, stream, made, _lib.cpattn_paged_append, "cpattn_paged_append", k.data_ptr(), ks,
-            v.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), pages, size, page_stride,
-            table_at, row, cu_at, kv_at, B, T, Hk, D, rope, rot, max_pos, 1 if interleaved else 0,
-            wq, wk, eps, _addr(q), qs, H, _addr(q_out), qos, _need_status(status, dev))
-    return q_out
+    return _binding.paged_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, rope_table,
+                                 interleaved, k_weight, eps, q, q_weight, q_out, status, stream)
 
 
-@functools.lru_cache(maxsize=256)
 def paged_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen):
     n = _lib.cpattn_paged_attn_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim,
                                               max_seqlen)
@@ -1030,37 +822,8 @@ def paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, max_seql
     sequence's new tokens and cache length.  Rows behind ``cu_seqlens[B]`` are
     not written.
     """
-    T, H, D = _shape_of(q, "q", 3, "[T, heads, D]")
-    dev = q.device
-    q_at = _need_flat(q, "q", _BF16, dev, (T, H, D))
-    Hk = _shape_of(k_cache, "k_cache", 4, "[num_pages, page_size, heads, D]")[2]
-    pages, size, page_stride, B, row, table_at, cu_at, kv_at = _need_cache(
-        k_cache, v_cache, page_table, cu_seqlens, kv_lens, dev, Hk, D)
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D)
-    made = []
-    if out is None:
-        out = torch.empty((T, H, D), dtype=_BF16, device=dev)
-        made.append(out)
-    else:
-        _need_flat(out, "out", _BF16, dev, (T, H, D))
-    if lse is None:
-        lse = torch.empty((T, H), dtype=_F32, device=dev)
-        made.append(lse)
-    else:
-        _need_flat(lse, "lse", _F32, dev, (T, H))
-    if workspace is None:
-        ws_bytes = paged_workspace_size(T, B, H, Hk, D, max_seqlen)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    else:
-        ws_bytes = workspace.numel()
-        _need_flat(workspace, "workspace", torch.uint8, dev, (ws_bytes,))
-    _run_on(dev, stream, made, _lib.cpattn_paged_attn, "cpattn_paged_attn", q_at,
-            k_cache.data_ptr(), v_cache.data_ptr(), pages, size, page_stride, table_at, row, cu_at,
-            kv_at, B, T, max_seqlen, max_kv_len, H, Hk, D, softmax_scale, 1 if causal else 0,
-            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes)
-    return out, lse
+    return _binding.paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, max_seqlen,
+                               max_kv_len, softmax_scale, causal, out, lse, workspace, stream)
 
 
 def poll_error(workspace, stream=None):

@@ -20,7 +20,6 @@
 // Everything between the load and the store is fp32 in registers, in packed
 // pairs, rounded to bf16 once.
 #include <cuda_bf16.h>
-#include <cstdlib>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -422,29 +421,29 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
   }
 }
 
-// Adds the CTAs' partial weight gradients: 8 warps share 32 features of one
-// weight, each taking every eighth row, and are added in a fixed order.
-__global__ void __launch_bounds__(256)
+// Adds the CTAs' partial weight gradients: 32 warps share 32 features of one
+// weight, each taking every 32nd row (a few hundred rows: two round trips of
+// eight loads), and are added in a fixed order.
+__global__ void __launch_bounds__(1024)
     norm_rope_dw_kernel(const float* partial, int q_rows, int rows, int D, float* dqw, float* dkw) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = D / 32;
   const bool is_k = static_cast<int>(blockIdx.x) >= per;
-  const int col = (static_cast<int>(blockIdx.x) - (is_k ? per : 0)) * 32 + lane;
+  const int col = (static_cast<int>(blockIdx.x) - (is_k ? per : 0)) * 32;
   const int r1 = is_k ? rows : q_rows;
   float s = 0.f;
 #pragma unroll 8
-  for (int r = (is_k ? q_rows : 0) + warp; r < r1; r += 8)
-    s += __ldcg(partial + static_cast<size_t>(r) * D + col);
+  for (int r = (is_k ? q_rows : 0) + warp; r < r1; r += 32)
+    s += __ldcg(partial + static_cast<size_t>(r) * D + col + lane);
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
-    float t = 0.f;
+  // Warp w adds the 32 sums of feature w.
+  float t = red[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += red[w][lane];
-    (is_k ? dkw : dqw)[col] = t;
-  }
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) (is_k ? dkw : dqw)[col + warp] = t;
 }
 
 template <int D, int NB>
@@ -474,15 +473,13 @@ static cudaError_t launch_norm_rope_d(const NormRopeParams& p, bool interleaved,
     const long long uq = (p.q_heads + run - 1) / run, uk = (p.kv_heads + run - 1) / run;
     return p.total_tokens * (uq + (p.page_table != nullptr ? 2 : 1) * uk);
   };
-  // Longer runs of heads share a position's angles and have more loads in
-  // flight, as long as they leave every SM several rounds of CTAs.
+  // Eight heads a lane group share a position's angles and have twice the loads
+  // in flight (16,384 tokens, 64 heads: 87 us, four heads 103 us), as long as
+  // they leave every SM several rounds of CTAs (32 tokens: four heads 6.1 us,
+  // eight 6.2 us).  Sixteen leave too few CTAs a SM (105 us).
   const long long many = 12LL * num_sms * (kNrThreads / (D / 8));
   if (units_at(1) == 0) return cudaSuccess;
-  const char* env = getenv("NB");
-  const int nb = env ? atoi(env) : units_at(2 * kUnit) >= many ? 2 : 1;
-  if (nb == 4)
-    return launch_norm_rope_t<D, 4>(p, interleaved, units_at(4 * kUnit), stream);
-  if (nb == 2)
+  if (units_at(2 * kUnit) >= many)
     return launch_norm_rope_t<D, 2>(p, interleaved, units_at(2 * kUnit), stream);
   return launch_norm_rope_t<D, 1>(p, interleaved, units_at(kUnit), stream);
 }
@@ -524,7 +521,7 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, f
   const bool any = p.total_tokens > 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * D / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

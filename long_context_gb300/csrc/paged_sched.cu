@@ -96,6 +96,107 @@ __device__ __forceinline__ int item_units(const PagedParams& p, const PagedItem&
 
 }  // namespace
 
+// Up to 32 sequences of one block of few rows each (a small decoding step): every
+// warp works out all splits in its lanes, without a barrier, and the warps share
+// the writing.
+__global__ void __launch_bounds__(128) paged_schedule_small_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int B = p.num_seqs;
+  int lo = 0, hi = 0, kv = 0;
+  if (lane < B) {
+    lo = p.cu_seqlens[lane];
+    hi = p.cu_seqlens[lane + 1];
+    kv = p.kv_lens[lane];
+  }
+  const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
+  const bool bad = lo < 0 || hi < lo || hi > p.total_q || hi - lo > p.max_seqlen || kv < 0 ||
+                   kv > p.max_kv_len || kv > cap || (lane == 0 && lo != 0);
+  if (__any_sync(0xffffffffu, bad)) {
+    if (threadIdx.x == 0) {
+      p.hdr->error = 1;  // CPATTN_ERR_INVALID_ARG
+      p.hdr->n_items = 0;
+      p.hdr->pad[0] = 0;
+    }
+    return;
+  }
+  const bool have = lane < B && hi > lo;
+  const int units = have ? (kv + p.shape.unit - 1) / p.shape.unit : 0;
+  const unsigned with = __ballot_sync(0xffffffffu, have);
+  long long all = units;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  const int lanes = __popc(with) * p.num_kv_heads;
+  const int share = 2 * lanes <= p.shape.round ? p.shape.round - lanes : p.shape.ctas;
+  long long target = (all * p.num_kv_heads + share - 1) / share;
+  if (target < p.shape.min_units) target = p.shape.min_units;
+  int n = have ? 1 : 0, per = units;
+  if (units > target) {
+    n = static_cast<int>((units + target - 1) / target);
+    per = (units + n - 1) / n;
+    n = (units + per - 1) / per;
+  }
+  // First split, slot and number among the split items, in one scan.
+  const long long mine = n + (n > 1 ? (static_cast<long long>(n) << 32) + (1ll << 48) : 0);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, incl, 31);
+  const long long before = incl - mine;
+  const int base = static_cast<int>(before & 0xffffffffll);
+  const int slot = n > 1 ? static_cast<int>((before >> 32) & 0xffff) : -1;
+  const int item = static_cast<int>(before >> 48);
+  const int splits = static_cast<int>(total & 0xffffffffll);
+  const int merges = static_cast<int>(total >> 48);
+  for (int e0 = threadIdx.x - lane; e0 < splits; e0 += 128) {
+    const int e = e0 + lane;
+    // The last lane whose first split is at most e (lanes without splits begin
+    // where the next one does, so the last is the owner).
+    int b = 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const int v = __shfl_sync(0xffffffffu, base, b + o);
+      const int first_n = __shfl_sync(0xffffffffu, n, b + o);
+      if (b + o < B && (v < e || (v == e && (first_n > 0 || v < splits)))) b += o;
+    }
+    PagedWork w;
+    w.tok0 = __shfl_sync(0xffffffffu, lo, b);
+    w.q_len = __shfl_sync(0xffffffffu, hi, b) - w.tok0;
+    w.kv_len = __shfl_sync(0xffffffffu, kv, b);
+    w.seq = b;
+    w.blk = 0;
+    const int s = e - __shfl_sync(0xffffffffu, base, b);
+    const int step = __shfl_sync(0xffffffffu, per, b);
+    w.kv_lo = s * step * p.shape.unit;
+    w.kv_hi = min(w.kv_len, (s + 1) * step * p.shape.unit);
+    w.slot0 = __shfl_sync(0xffffffffu, slot, b);
+    w.slot = w.slot0 < 0 ? -1 : w.slot0 + s;
+    w.n = __shfl_sync(0xffffffffu, n, b);
+    w.item = __shfl_sync(0xffffffffu, item, b);
+    w.pad = 0;
+    if (e < splits) p.work[e] = w;
+  }
+  if (p.shape.join) {
+    for (int i = threadIdx.x; i < merges * p.num_kv_heads; i += 128) p.arrived[i] = 0;
+  } else if (threadIdx.x < 32 && n > 1) {
+    PagedMerge m = {};
+    m.tok0 = lo;
+    m.q_len = hi - lo;
+    m.blk = 0;
+    m.slot0 = slot;
+    m.n = n;
+    p.merge[item] = m;
+  }
+  if (threadIdx.x == 0) {
+    p.hdr->error = 0;
+    p.hdr->n_items = splits;
+    p.hdr->pad[0] = merges;
+  }
+}
+
 // NT threads; batches of up to 128 items take 128, whose barriers are quicker.
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p) {
@@ -307,7 +408,10 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
 }
 
 cudaError_t launch_paged_schedule(const PagedParams& p, cudaStream_t stream) {
-  if (p.total_q * p.group / p.shape.rows + p.num_seqs <= 128)
+  if (!p.shape.tiles && p.num_seqs <= 32 &&
+      static_cast<long long>(p.max_seqlen) * p.group <= p.shape.rows)
+    paged_schedule_small_kernel<<<1, 128, 0, stream>>>(p);
+  else if (p.total_q * p.group / p.shape.rows + p.num_seqs <= 128)
     paged_schedule_kernel<128><<<1, 128, 0, stream>>>(p);
   else
     paged_schedule_kernel<1024><<<1, 1024, 0, stream>>>(p);
