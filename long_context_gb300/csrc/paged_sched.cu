@@ -153,15 +153,12 @@ __global__ void __launch_bounds__(128) paged_schedule_small_kernel(const PagedPa
   const int merges = static_cast<int>(total >> 48);
   for (int e0 = threadIdx.x - lane; e0 < splits; e0 += 128) {
     const int e = e0 + lane;
-    // The last lane whose first split is at most e (lanes without splits begin
-    // where the next one does, so the last is the owner).
+    // The last lane whose first split is at most e (a lane without splits begins
+    // where the next one with some does, and behind the last at `splits`).
     int b = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const int v = __shfl_sync(0xffffffffu, base, b + o);
-      const int first_n = __shfl_sync(0xffffffffu, n, b + o);
-      if (b + o < B && (v < e || (v == e && (first_n > 0 || v < splits)))) b += o;
-    }
+    for (int o = 16; o > 0; o >>= 1)
+      if (__shfl_sync(0xffffffffu, base, b + o) <= e) b += o;
     PagedWork w;
     w.tok0 = __shfl_sync(0xffffffffu, lo, b);
     w.q_len = __shfl_sync(0xffffffffu, hi, b) - w.tok0;
