@@ -17,8 +17,13 @@
 //                   barrier; it also clears what the last V tile holds behind
 //                   the cache's end (weight 0 times a NaN there would be NaN)
 //   warp  11        idle
-// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 and O1 at 256 + t*D; P_t
-// (bf16, two per column) overwrites the first 64 columns of S_t.
+// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 and O1 at 256 + t*D.  P_t
+// (bf16, two per column) overwrites the first 64 columns of S_t at head size
+// 128, so S of the next key tile follows PV of this one and a Q tile's chain is
+// softmax, hand-over, PV and S (about 2,900 cycles a key tile, of which the
+// tensor pipe works 2,048 for two Q tiles).  At head size 64 the columns suffice
+// for a P of its own (384 + t*64): the softmax hands S back once it is in
+// registers and the next S is computed during the exponentials.
 //
 // Softmax: p = 2^(s scale log2 e - m) with a running reference m per row that
 // only has to keep p below 2^16 (O and l share it, so O / l and m + ln l do not
@@ -52,12 +57,17 @@ struct TileCfg {
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kBarOff = kVOff + kStages * kTileBytes;
   // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[NQ],
-  // p_full[NQ], o_done[NQ], drain, staged[NQ]
-  static constexpr int kNumBars = 1 + 4 * kStages + 3 * kNQ + 1 + kNQ;
+  // p_full[NQ], o_done[NQ], drain, staged[NQ], s_read[NQ]
+  static constexpr int kNumBars = 1 + 4 * kStages + 3 * kNQ + 1 + 2 * kNQ;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;  // + align slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 2 * kBN;
+  // Head size 64 leaves TMEM columns for a P of its own, so that S is free as
+  // soon as the softmax has read it.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kPCol = kOwnP ? kOCol + kNQ * D : 0;
+  static constexpr uint32_t kPStep = kOwnP ? kBN / 2 : kBN;
 };
 
 // Byte offset of 16-byte chunk c of row r in a tile stored as 64-column
@@ -125,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_done = p_full + kNQ;
   uint64_t* drain = o_done + kNQ;
   uint64_t* staged = drain + 1;  // O tile t staged in shared memory (128 arrivals)
+  uint64_t* s_read = staged + kNQ;  // kOwnP: S_t is in registers (128 arrivals)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
 
@@ -173,7 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&o_done[t], 1);
       }
       mbar_init(drain, 1);
-      for (int t = 0; t < kNQ; ++t) mbar_init(&staged[t], kBM);
+      for (int t = 0; t < kNQ; ++t) {
+        mbar_init(&staged[t], kBM);
+        mbar_init(&s_read[t], kBM);
+      }
       *abort_flag = 0;
       fence_mbarrier_init();
       tma_prefetch_desc(&tm_q);
@@ -274,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto issue_pv = [&](int t, int st, bool acc) {
         const uint32_t d = tmem + C::kOCol + t * D;
-        const uint32_t a = tmem + t * kBN;
+        const uint32_t a = tmem + C::kPCol + t * C::kPStep;
         const uint32_t b0 = lo_v + st * (C::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
@@ -292,6 +306,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = x % C::kStages;
         const bool has_next = x + 1 < n;
         const int st1 = (x + 1) % C::kStages;
+        if (C::kOwnP) {
+          if (has_next) {
+            for (int t = 0; t < nq; ++t) {
+              named_bar_sync(1, 64);  // S_t(x) was read and K(x+1) is ready
+              if (lane == 0) {
+                tc_fence_after();
+                issue_s(t, st1);
+                if (t == nq - 1) mma_commit(&k_empty[st1]);
+              }
+              __syncwarp();
+            }
+          }
+          for (int t = 0; t < nq; ++t) {
+            named_bar_sync(1, 64);  // P_t(x) and V(x) are ready
+            if (lane == 0) {
+              tc_fence_after();
+              issue_pv(t, st, x > 0);
+              mma_commit(&o_done[t]);  // every tile: P_t may be overwritten
+              if (t == nq - 1) mma_commit(&v_empty[st]);
+            }
+            __syncwarp();
+          }
+          continue;
+        }
         for (int t = 0; t < nq; ++t) {
           named_bar_sync(1, 64);  // P_t(x), V(x) and K(x+1) are ready
           if (lane == 0) {
@@ -328,6 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ph = (x / C::kStages) & 1;
         const int st1 = (x + 1) % C::kStages;
         const uint32_t ph1 = ((x + 1) / C::kStages) & 1;
+        if (C::kOwnP && x + 1 < n) {
+          if (lane == 0 && ok) ok = wait_bounded(&k_full[st1], ph1, abort_flag);
+          for (int t = 0; t < nq; ++t) {
+            if (lane == 0 && ok) ok = wait_bounded(&s_read[t], x & 1, abort_flag);
+            __syncwarp();
+            named_bar_sync(1, 64);
+          }
+        }
         for (int t = 0; t < nq; ++t) {
           if (t == 0) {
             if (lane == 0 && ok) ok = wait_bounded(&v_full[st], ph, abort_flag);
@@ -344,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
-            if (lane == 0 && ok && x + 1 < n) ok = wait_bounded(&k_full[st1], ph1, abort_flag);
+            if (!C::kOwnP && lane == 0 && ok && x + 1 < n)
+              ok = wait_bounded(&k_full[st1], ph1, abort_flag);
           }
           if (lane == 0 && ok) ok = wait_bounded(&p_full[t], x & 1, abort_flag);
           __syncwarp();
@@ -366,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t s_addr = tmem + lane_base + t * kBN;
       const uint32_t o_addr = tmem + lane_base + C::kOCol + t * D;
+      const uint32_t p_addr = tmem + lane_base + C::kPCol + t * C::kPStep;
       const int my_tok = tok_lo + t * tile_toks + r / G;
       const bool row_valid = r < tile_rows && my_tok >= 0;
       // Keys below lim are visible; a row that is not there sees none, and
@@ -380,8 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bounded(&s_full[t], x & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        // S is still in TMEM for a second pass: P is written after it.
-        bool with_max = __any_sync(0xffffffffu, m_run == kNegInfT);
+        // S is still in TMEM for a second pass: P is written after it.  With a P
+        // of its own S is given back before the exponentials, so there the
+        // maximum is always taken.
+        bool with_max = C::kOwnP || __any_sync(0xffffffffu, m_run == kNegInfT);
         float2 acc0, acc1;
         uint32_t pk[kBN / 2];
 #pragma unroll 1
@@ -392,6 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < kBN / 32; ++q) reg_fence32(sr + q * 32);
+          if (C::kOwnP) {
+            tc_fence_before();
+            mbar_arrive(&s_read[t]);
+          }
 
           // Visible keys of this row form a prefix of the tile.
           const int nvis = lim - (kv_lo + x * kBN);
@@ -416,9 +470,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m_new = fmaxf(m_run, m_tile);
             if (__any_sync(0xffffffffu, m_new > m_run + kMoveByT)) {
               const float alpha = (m_run == kNegInfT) ? 0.f : ex2_approx(m_run - m_new);
+              if (C::kOwnP && x > 0) {
+                ok = __all_sync(0xffffffffu, wait_bounded(&o_done[t], (x - 1) & 1, abort_flag));
+                tc_fence_after();
+              }
               if (x > 0) {
-                // PV of the previous tile completed before S of this one (same
-                // issuing thread, committed in order), so O_t is stable here.
+                // PV of the previous tile has completed: it was waited for, or
+                // came before S of this one (same issuing thread, committed in
+                // order).  O_t is stable here.
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                   uint32_t orr[32];
@@ -454,14 +513,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           with_max = true;
         }
         l_run += (acc0.x + acc1.x) + (acc0.y + acc1.y);
-        tmem_st32(s_addr, pk);
-        tmem_st32(s_addr + 32, pk + 32);
+        if (C::kOwnP && x > 0) {  // PV of the previous tile has read P
+          ok = __all_sync(0xffffffffu,
+                          ok && wait_bounded(&o_done[t], (x - 1) & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st32(p_addr, pk);
+        tmem_st32(p_addr + 32, pk + 32);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[t]);
       }
       if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, wait_bounded(&o_done[t], 0, abort_flag));
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded(&o_done[t], C::kOwnP ? (n - 1) & 1 : 0, abort_flag));
         tc_fence_after();
       }
       if (ok) {
