@@ -10,13 +10,15 @@
 //
 // The organisation is the ring-attention forward's (attn_fwd.cu):
 //   warps 0-3, 4-7  softmax for Q tile 0, 1 (thread = row = TMEM lane)
-//   warp  8         TMA producer (Q once, then K/V through a stage ring)
+//   warp  8, 11     TMA producers: Q once and K, V, through stage rings (pages
+//                   of 16 tokens make eight or sixteen copies of a tile; one warp
+//                   issuing both took 1,069 us for 4,864 tokens over 32,768,
+//                   16 heads of 128, and two take 908, as with larger pages)
 //   warp  9         MMA issuer (one thread) and TMEM owner
 //   warp  10        waits for the MMA issuer, which an mbarrier wait would stall
 //                   until its queued MMAs drain, and releases it through a named
 //                   barrier; it also clears what the last V tile holds behind
 //                   the cache's end (weight 0 times a NaN there would be NaN)
-//   warp  11        idle
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 and O1 at 256 + t*D.  P_t
 // (bf16, two per column) overwrites the first 64 columns of S_t at head size
 // 128, so S of the next key tile follows PV of this one and a Q tile's chain is
@@ -220,10 +222,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     regs_lower_56();
-    if (warp == 8) {
-      // ------------------------------------------------------ TMA producer --
+    if (warp == 8 || warp == 11) {
+      // ------------------------------ TMA producers: warp 8 K, warp 11 V --
+      const bool is_k = warp == 8;
       const uint64_t pol_kv = l2_policy_evict_last();
-      int nk = min(n, 1), nv = nk;  // K and V tiles whose copies were issued
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      uint8_t* ring = smem + (is_k ? C::kKOff : C::kVOff);
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      int issued = min(n, 1);  // tiles whose copies were issued
       bool ok = true;
       int next_page = n > 1 ? page_of(kv_lo + kBN) : -1;
       for (int x = 1; x < n; ++x) {
@@ -232,14 +239,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kv0 = kv_lo + x * kBN;
         const int page = next_page;
         if (x + 1 < n) next_page = page_of(kv0 + kBN);
-        ok = __all_sync(0xffffffffu, wait_bounded(&k_empty[st], ph ^ 1, abort_flag));
+        ok = __all_sync(0xffffffffu, wait_bounded(&empty[st], ph ^ 1, abort_flag));
         if (!ok) break;
-        copy_tile(&tm_k, smem + C::kKOff + st * C::kTileBytes, &k_full[st], kv0, page, pol_kv);
-        ++nk;
-        ok = __all_sync(0xffffffffu, wait_bounded(&v_empty[st], ph ^ 1, abort_flag));
-        if (!ok) break;
-        copy_tile(&tm_v, smem + C::kVOff + st * C::kTileBytes, &v_full[st], kv0, page, pol_kv);
-        ++nv;
+        copy_tile(map, ring + st * C::kTileBytes, &full[st], kv0, page, pol_kv);
+        ++issued;
       }
       if (lane == 0) {
         if (!ok) {
@@ -247,17 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           *abort_flag = 1;
         }
         // Drain: every copy issued into shared memory must land before exit.
-        drain_wait(q_full, 0);
-        for (int st = 0; st < C::kStages; ++st) {
-          if (st < nk) {
-            const int last = st + ((nk - 1 - st) / C::kStages) * C::kStages;
-            drain_wait(&k_full[st], (last / C::kStages) & 1);
+        if (is_k) drain_wait(q_full, 0);
+        for (int st = 0; st < C::kStages; ++st)
+          if (st < issued) {
+            const int last = st + ((issued - 1 - st) / C::kStages) * C::kStages;
+            drain_wait(&full[st], (last / C::kStages) & 1);
           }
-          if (st < nv) {
-            const int last = st + ((nv - 1 - st) / C::kStages) * C::kStages;
-            drain_wait(&v_full[st], (last / C::kStages) & 1);
-          }
-        }
       }
       __syncwarp();
     } else if (warp == 9) {
