@@ -244,7 +244,7 @@ struct NormRopeBwdParams {
   int q_ctas;      // CTAs that take the query heads (set by the launch)
 };
 
-cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, float* dqw,
+cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, bool interleaved, float* dqw,
                                  float* dkw, int num_sms, cudaStream_t stream);
 
 // Attention over a paged KV cache (paged_*.cu).  A row is one (token, query

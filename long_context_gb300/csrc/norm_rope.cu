@@ -30,8 +30,6 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kUnit = 4;     // heads of one batch of copies
-constexpr int kBwdUnit = 4;  // backward
-constexpr int kBwdSmem = 2 * 2 * kBwdUnit * kNrThreads * 16;
 constexpr int kErrArg = 1;   // CPATTN_ERR_INVALID_ARG
 
 // Four bf16 values as two packed pairs of floats.
@@ -269,16 +267,16 @@ __global__ void __launch_bounds__(kNrThreads, PAGED ? 4 : 5) norm_rope_kernel(co
   }
 }
 
-// Gradients.  A fixed number of CTAs walk the units (kBwdUnit heads of one
-// token): the first q_ctas take the query heads, the others the key heads, so
+// Gradients.  A fixed number of CTAs walk the units (RUN batches of UNIT heads
+// of one token): the first q_ctas take the query heads, the others the key heads, so
 // a lane holds one weight's 8 features and their sums of g hat in registers.
 // The CTA adds its lane groups in shared memory and norm_rope_dw_kernel adds
 // the CTAs' rows: the same order in every run, no atomics.
-template <int D, bool INTERLEAVED>
+template <int D, bool INTERLEAVED, int UNIT, int RUN>
 __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int LG = D / 8;
   constexpr int kGroups = kNrThreads / LG;
-  extern __shared__ __align__(16) uint8_t ring[];  // [2][gradients, inputs][kBwdUnit][threads] x 16
+  extern __shared__ __align__(16) uint8_t ring[];  // [2][gradients, inputs][UNIT][threads] x 16
   __shared__ __align__(16) float red[kGroups][D];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
   const int cta = static_cast<int>(blockIdx.x) - (is_k ? p.q_ctas : 0);
   const int ctas = is_k ? static_cast<int>(gridDim.x) - p.q_ctas : p.q_ctas;
   const int heads = is_k ? p.kv_heads : p.q_heads;
-  const int upt = (heads + kBwdUnit - 1) / kBwdUnit;  // units of a token
+  const int upt = (heads + RUN * UNIT - 1) / (RUN * UNIT);  // units of a token
   const long long units = p.total_tokens * upt;
   const __nv_bfloat16* xin = is_k ? p.k : p.q;
   const __nv_bfloat16* gin = is_k ? p.dk_out : p.dq_out;
@@ -309,8 +307,9 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
     unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.hi)), wb);
   }
   const long long stride = static_cast<long long>(ctas) * kGroups;
-  // A unit is kBwdUnit heads of one token.  The next unit's rows are copied
-  // to shared memory while the current unit's are used.  Whole warps stay in the loop together (the shuffles are warp-wide).
+  // The next batch's rows (of this unit or the next) are copied to shared memory
+  // while the current one's are used; a unit's batches share its angles.  Whole
+  // warps stay in the loop together (the shuffles are warp-wide).
   struct Place {
     int token, h0, end, pos;
   };
@@ -318,23 +317,23 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
     Place a = {0, 0, 0, 0};
     if (u < units) {
       a.token = static_cast<int>(static_cast<unsigned>(u) / upt);
-      a.h0 = static_cast<int>(static_cast<unsigned>(u) - a.token * upt) * kBwdUnit;
-      a.end = min(a.h0 + kBwdUnit, heads);
+      a.h0 = static_cast<int>(static_cast<unsigned>(u) - a.token * upt) * (RUN * UNIT);
+      a.end = min(a.h0 + RUN * UNIT, heads);
       if (turning) a.pos = __ldg(p.positions + a.token);
     }
     return a;
   };
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
   const uint8_t* row = ring + (threadIdx.x - c) * 16;
-  auto load = [&](const Place& a, int buf) {
+  auto load = [&](const Place& a, int h0, int buf) {
 #pragma unroll
-    for (int u = 0; u < kBwdUnit; ++u) {
-      const int h = a.h0 + u;
-      const uint32_t dst = mine + (buf * 2 * kBwdUnit + u) * (kNrThreads * 16);
+    for (int u = 0; u < UNIT; ++u) {
+      const int h = h0 + u;
+      const uint32_t dst = mine + (buf * 2 * UNIT + u) * (kNrThreads * 16);
       if (h < a.end) {
         cp_async16(dst, gin + a.token * g_stride + h * D + c * 8, 16);
         if (normed)
-          cp_async16(dst + kBwdUnit * (kNrThreads * 16), xin + a.token * x_stride + h * D + c * 8,
+          cp_async16(dst + UNIT * (kNrThreads * 16), xin + a.token * x_stride + h * D + c * 8,
                      16);
       }
     }
@@ -342,12 +341,11 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
   };
   long long unit = static_cast<long long>(cta) * kGroups + group;
   Place at = place(unit);
-  load(at, 0);
+  load(at, at.h0, 0);
   int buf = 0;
   for (long long base = static_cast<long long>(cta) * kGroups; base < units; base += stride) {
     unit += stride;
     const Place ahead = place(unit);
-    load(ahead, buf ^ 1);
     bool ok = at.end > 0;
     if (turning) {
       const bool good = at.pos >= 0 && at.pos < p.max_pos;
@@ -356,55 +354,60 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
     }
     load_turn<INTERLEAVED>(t, p.table + static_cast<size_t>(ok ? at.pos : 0) * p.rot, p.rot, c, ok,
                            -1.f);
-    cp_async_wait<1>();
-    __syncwarp();
 #pragma unroll
-    for (int u = 0; u < kBwdUnit; ++u) {
-      const int h = at.h0 + u;
-      const bool count = ok && h < at.end;
-      const uint8_t* piece = row + (buf * 2 * kBwdUnit + u) * (kNrThreads * 16);
-      float2 a[2], b[2];
-      unpack4(*reinterpret_cast<const uint2*>(piece + t.lo * 2), a);
-      unpack4(*reinterpret_cast<const uint2*>(piece + t.hi * 2), b);
-      apply_turn<INTERLEAVED>(t, a, b);  // g
-      if (normed) {
-        const uint8_t* px = piece + kBwdUnit * (kNrThreads * 16);
-        float2 xa[2], xb[2];
-        unpack4(*reinterpret_cast<const uint2*>(px + t.lo * 2), xa);
-        unpack4(*reinterpret_cast<const uint2*>(px + t.hi * 2), xb);
-        float2 ss = both2(0.f), dot = both2(0.f);
+    for (int j = 0; j < RUN; ++j) {
+      if (j + 1 < RUN) load(at, at.h0 + (j + 1) * UNIT, buf ^ 1);
+      else load(ahead, ahead.h0, buf ^ 1);
+      cp_async_wait<1>();
+      __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ss = __ffma2_rn(xa[k], xa[k], ss);
-          ss = __ffma2_rn(xb[k], xb[k], ss);
-          dot = __ffma2_rn(__fmul2_rn(a[k], wa[k]), xa[k], dot);
-          dot = __ffma2_rn(__fmul2_rn(b[k], wb[k]), xb[k], dot);
-        }
-        const float sum = row_sum<LG>(ss.x + ss.y);
-        const float prod = row_sum<LG>(dot.x + dot.y);
-        const float r = rsqrtf(sum * (1.f / D) + p.eps);
-        const float2 r2 = both2(r);
-        const float2 m2 = both2(-prod * r * (1.f / D));  // -mean(u hat)
+      for (int u = 0; u < UNIT; ++u) {
+        const int h = at.h0 + j * UNIT + u;
+        const bool count = ok && h < at.end;
+        const uint8_t* piece = row + (buf * 2 * UNIT + u) * (kNrThreads * 16);
+        float2 a[2], b[2];
+        unpack4(*reinterpret_cast<const uint2*>(piece + t.lo * 2), a);
+        unpack4(*reinterpret_cast<const uint2*>(piece + t.hi * 2), b);
+        apply_turn<INTERLEAVED>(t, a, b);  // g
+        if (normed) {
+          const uint8_t* px = piece + UNIT * (kNrThreads * 16);
+          float2 xa[2], xb[2];
+          unpack4(*reinterpret_cast<const uint2*>(px + t.lo * 2), xa);
+          unpack4(*reinterpret_cast<const uint2*>(px + t.hi * 2), xb);
+          float2 ss = both2(0.f), dot = both2(0.f);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 ha = __fmul2_rn(xa[k], r2), hb = __fmul2_rn(xb[k], r2);
-          if (count) {
-            dwa[k] = __ffma2_rn(a[k], ha, dwa[k]);
-            dwb[k] = __ffma2_rn(b[k], hb, dwb[k]);
+          for (int k = 0; k < 2; ++k) {
+            ss = __ffma2_rn(xa[k], xa[k], ss);
+            ss = __ffma2_rn(xb[k], xb[k], ss);
+            dot = __ffma2_rn(__fmul2_rn(a[k], wa[k]), xa[k], dot);
+            dot = __ffma2_rn(__fmul2_rn(b[k], wb[k]), xb[k], dot);
           }
-          a[k] = __fmul2_rn(__ffma2_rn(ha, m2, __fmul2_rn(a[k], wa[k])), r2);
-          b[k] = __fmul2_rn(__ffma2_rn(hb, m2, __fmul2_rn(b[k], wb[k])), r2);
+          const float sum = row_sum<LG>(ss.x + ss.y);
+          const float prod = row_sum<LG>(dot.x + dot.y);
+          const float r = rsqrtf(sum * (1.f / D) + p.eps);
+          const float2 r2 = both2(r);
+          const float2 m2 = both2(-prod * r * (1.f / D));  // -mean(u hat)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 ha = __fmul2_rn(xa[k], r2), hb = __fmul2_rn(xb[k], r2);
+            if (count) {
+              dwa[k] = __ffma2_rn(a[k], ha, dwa[k]);
+              dwb[k] = __ffma2_rn(b[k], hb, dwb[k]);
+            }
+            a[k] = __fmul2_rn(__ffma2_rn(ha, m2, __fmul2_rn(a[k], wa[k])), r2);
+            b[k] = __fmul2_rn(__ffma2_rn(hb, m2, __fmul2_rn(b[k], wb[k])), r2);
+          }
+        }
+        if (count) {
+          __nv_bfloat16* dst = out + at.token * o_stride + h * D;
+          *reinterpret_cast<uint2*>(dst + t.lo) = pack4(a);
+          *reinterpret_cast<uint2*>(dst + t.hi) = pack4(b);
         }
       }
-      if (count) {
-        __nv_bfloat16* dst = out + at.token * o_stride + h * D;
-        *reinterpret_cast<uint2*>(dst + t.lo) = pack4(a);
-        *reinterpret_cast<uint2*>(dst + t.hi) = pack4(b);
-      }
+      __syncwarp();  // the buffer is refilled by all lanes
+      buf ^= 1;
     }
-    __syncwarp();  // the buffer is refilled by all lanes
     at = ahead;
-    buf ^= 1;
   }
   if (!normed) return;
 #pragma unroll
@@ -490,11 +493,13 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int D, bool interleaved, i
                  : launch_norm_rope_d<128>(p, interleaved, num_sms, stream);
 }
 
-cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, float* dqw,
-                                 float* dkw, int num_sms, cudaStream_t stream) {
+template <int D, int UNIT, int RUN>
+static cudaError_t launch_norm_rope_bwd_t(NormRopeBwdParams p, bool interleaved, float* dqw,
+                                          float* dkw, int num_sms, cudaStream_t stream) {
+  constexpr int kSmem = 2 * 2 * UNIT * kNrThreads * 16;
+  constexpr int kHeads = RUN * UNIT;
   const int groups = kNrThreads / (D / 8);
-  const long long uq = (p.q_heads + kBwdUnit - 1) / kBwdUnit;
-  const long long uk = (p.kv_heads + kBwdUnit - 1) / kBwdUnit;
+  const long long uq = (p.q_heads + kHeads - 1) / kHeads, uk = (p.kv_heads + kHeads - 1) / kHeads;
   const long long needed = (p.total_tokens * (uq + uk) + groups - 1) / groups;
   // Three CTAs a SM, shared out by the number of heads; at least one for each.
   long long grid = num_sms * 3LL < kNormRopeBwdCtas ? num_sms * 3LL : kNormRopeBwdCtas;
@@ -505,14 +510,11 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, f
   p.q_ctas = static_cast<int>(gq);
   const unsigned g = static_cast<unsigned>(grid);
   if (p.total_tokens > 0) {
-    auto kern = D == 64 ? (interleaved ? norm_rope_bwd_kernel<64, true>
-                                       : norm_rope_bwd_kernel<64, false>)
-                        : (interleaved ? norm_rope_bwd_kernel<128, true>
-                                       : norm_rope_bwd_kernel<128, false>);
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    auto kern = interleaved ? norm_rope_bwd_kernel<D, true, UNIT, RUN>
+                            : norm_rope_bwd_kernel<D, false, UNIT, RUN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<g, kNrThreads, kBwdSmem, stream>>>(p);
+    kern<<<g, kNrThreads, kSmem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -530,6 +532,22 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdParams p, int D, bool interleaved, f
   cfg.numAttrs = any ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(p.partial),
                             any ? p.q_ctas : 0, any ? static_cast<int>(g) : 0, D, dqw, dkw);
+}
+
+cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, bool interleaved, float* dqw,
+                                 float* dkw, int num_sms, cudaStream_t stream) {
+  // Runs of eight heads (four batches of two) share a position's angles and the
+  // unit's bookkeeping: 16,384 tokens of 64 heads 125 us, runs of two 171 us,
+  // two batches of four 133 us.  They have to leave every lane group four units
+  // or the groups even out badly: 4,999 tokens of 20 heads 18.4 us, runs of two
+  // 16.4 us.
+  const long long groups = 3LL * num_sms * (kNrThreads / (D / 8));
+  const bool many = p.total_tokens * ((p.q_heads + 7) / 8 + (p.kv_heads + 7) / 8) >= 4 * groups;
+  if (D == 64)
+    return many ? launch_norm_rope_bwd_t<64, 2, 4>(p, interleaved, dqw, dkw, num_sms, stream)
+                : launch_norm_rope_bwd_t<64, 2, 1>(p, interleaved, dqw, dkw, num_sms, stream);
+  return many ? launch_norm_rope_bwd_t<128, 2, 4>(p, interleaved, dqw, dkw, num_sms, stream)
+              : launch_norm_rope_bwd_t<128, 2, 1>(p, interleaved, dqw, dkw, num_sms, stream);
 }
 
 }  // namespace cpattn
