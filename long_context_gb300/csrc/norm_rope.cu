@@ -29,7 +29,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kUnit = 4;     // heads of one batch of copies
+constexpr int kUnit = 2;    // heads of one batch of copies
 constexpr int kErrArg = 1;   // CPATTN_ERR_INVALID_ARG
 
 // Four bf16 values as two packed pairs of floats.
@@ -236,7 +236,10 @@ __global__ void __launch_bounds__(kNrThreads, PAGED ? 4 : 5) norm_rope_kernel(co
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     // This batch's rows have landed, every lane's part of them.
-    if (nb == 0) cp_async_wait<NB - 1>(); else cp_async_wait<0>();
+    if (nb == 0) cp_async_wait<NB - 1>();
+    else if (nb == 1) cp_async_wait<(NB > 2 ? NB - 2 : 0)>();
+    else if (nb == 2) cp_async_wait<(NB > 3 ? NB - 3 : 0)>();
+    else cp_async_wait<0>();
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
@@ -460,11 +463,7 @@ static cudaError_t launch_norm_rope_t(const NormRopeParams& p, bool interleaved,
                                    : norm_rope_kernel<D, false, true, NB>)
                     : (interleaved ? norm_rope_kernel<D, true, false, NB>
                                    : norm_rope_kernel<D, false, false, NB>);
-  if (kSmem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-  }
+  static_assert(kSmem <= 48 * 1024, "no opt-in needed");
   kern<<<grid, kNrThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -476,12 +475,15 @@ static cudaError_t launch_norm_rope_d(const NormRopeParams& p, bool interleaved,
     const long long uq = (p.q_heads + run - 1) / run, uk = (p.kv_heads + run - 1) / run;
     return p.total_tokens * (uq + (p.page_table != nullptr ? 2 : 1) * uk);
   };
-  // Eight heads a lane group share a position's angles and have twice the loads
-  // in flight (16,384 tokens, 64 heads: 87 us, four heads 103 us), as long as
-  // they leave every SM several rounds of CTAs (32 tokens: four heads 6.1 us,
-  // eight 6.2 us).  Sixteen leave too few CTAs a SM (105 us).
+  // Eight heads a lane group share a position's angles and have four times the
+  // loads in flight of two (16,384 tokens of 64 heads: 87 us, four heads 103 us,
+  // sixteen 92 us), as long as they leave every SM several rounds of CTAs; a
+  // decoding step wants its few rows spread out (32 tokens of 40 heads: two heads
+  // 4.8 us, four 6.1 us).
   const long long many = 12LL * num_sms * (kNrThreads / (D / 8));
   if (units_at(1) == 0) return cudaSuccess;
+  if (units_at(4 * kUnit) >= many)
+    return launch_norm_rope_t<D, 4>(p, interleaved, units_at(4 * kUnit), stream);
   if (units_at(2 * kUnit) >= many)
     return launch_norm_rope_t<D, 2>(p, interleaved, units_at(2 * kUnit), stream);
   return launch_norm_rope_t<D, 1>(p, interleaved, units_at(kUnit), stream);
