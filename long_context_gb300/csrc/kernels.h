@@ -283,7 +283,8 @@ struct PagedShape {
   bool tiles;      // the tensor-memory kernel (else the register kernel)
   int rows;        // rows of a block
   int unit;        // keys of a unit
-  int min_units;   // an item is split only above this many units
+  int min_units;   // a split is not made for less than so many units
+  int whole;       // items of up to so many units stay whole
   int ctas;        // a split does at least 1 / ctas of the whole work
   int round;       // CTAs resident at once (at most ctas)
   bool join;       // the last CTA of a split item joins it (else a merge kernel)

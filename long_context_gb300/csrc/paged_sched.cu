@@ -10,7 +10,7 @@
 // Tiles (one CTA a SM, an item is up to hundreds of units): the items' units are
 // laid end to end and cut at every multiple of one SM's share
 // C = max(min_units, ceil(W heads / SMs)), unless the cut would fall within C / 16
-// of an item's end or the item has at most min_units (or, when an eighth of the
+// of an item's end or the item has at most eight units (or, when an eighth of the
 // work is in items of less than C / 4, at most C).  So items that divide badly among the SMs are evened out by
 // at most one cut a SM, and the splits are listed by decreasing size, which the
 // hardware then starts in that order as SMs become free.  (2,048 tokens over
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   const int snap = target / 16 + 1;
   // Tiles: when small items hold an eighth of the work, they even out the SMs
   // by themselves (started last), and only items above a share are cut.
-  int uncut = p.shape.min_units;  // items of at most so many units stay whole
+  int uncut = p.shape.whole;  // items of at most so many units stay whole
   if (tiles) {
     long long small_sum = 0;
     __syncthreads();

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = x % C::kStages;
         const bool has_next = x + 1 < n;
         const int st1 = (x + 1) % C::kStages;
-        if (C::kOwnP) {
+        if constexpr (C::kOwnP) {
           if (has_next) {
             for (int t = 0; t < nq; ++t) {
               named_bar_sync(1, 64);  // S_t(x) was read and K(x+1) is ready
@@ -326,21 +326,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          continue;
-        }
-        for (int t = 0; t < nq; ++t) {
-          named_bar_sync(1, 64);  // P_t(x), V(x) and K(x+1) are ready
-          if (lane == 0) {
-            tc_fence_after();
-            issue_pv(t, st, x > 0);
-            if (!has_next) mma_commit(&o_done[t]);
-            if (t == nq - 1) mma_commit(&v_empty[st]);
-            if (has_next) {
-              issue_s(t, st1);
-              if (t == nq - 1) mma_commit(&k_empty[st1]);
+        } else {
+          for (int t = 0; t < nq; ++t) {
+            named_bar_sync(1, 64);  // P_t(x), V(x) and K(x+1) are ready
+            if (lane == 0) {
+              tc_fence_after();
+              issue_pv(t, st, x > 0);
+              if (!has_next) mma_commit(&o_done[t]);
+              if (t == nq - 1) mma_commit(&v_empty[st]);
+              if (has_next) {
+                issue_s(t, st1);
+                if (t == nq - 1) mma_commit(&k_empty[st1]);
+              }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       if (lane == 0) {

@@ -63,13 +63,16 @@ PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
   if (s.tiles) {
     s.rows = kNQ * static_cast<int>(kBM / group * group);
     s.unit = kBN;
-    s.min_units = 8;
+    // A key tile takes 1.5 us and a cut costs about 6 us (the merge): pieces of
+    // four tiles pay for items above eight.
+    s.min_units = 4;
+    s.whole = 8;
     s.ctas = 152;
     s.round = 152;
   } else {
     s.rows = rows <= 16 ? 16 : 32;
     s.unit = 64;
-    s.min_units = 1;
+    s.min_units = s.whole = 1;
     s.ctas = 608;
     s.round = 304;
   }
@@ -447,8 +450,8 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   } else if (launch_paged_rows(p, head_dim, s) != cudaSuccess) {
     return CPATTN_ERR_CUDA;
   }
-  // An item of no more than min_units units is never split.
-  if (!p.shape.join && max_kv_len > p.shape.min_units * p.shape.unit &&
+  // Short items are never split.
+  if (!p.shape.join && max_kv_len > p.shape.whole * p.shape.unit &&
       launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   return CPATTN_OK;
