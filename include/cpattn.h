@@ -460,8 +460,9 @@ int cpattn_fwd_noalloc(const void* q, const void* k, const void* v,
  *                 dq may be dq_out, and dk dk_out (in place).
  *   dq_weight, dk_weight  float [D], written whole (NULL without weights).
  *   workspace     >= cpattn_qk_norm_rope_bwd_workspace_size(D) bytes, 256-byte
- *                 aligned (NULL without weights).  Sums are taken in a fixed
- *                 order: equal inputs give equal bits.
+ *                 aligned (NULL without weights); calls that may overlap need
+ *                 one each.  Sums are taken in a fixed order: equal inputs give
+ *                 equal bits.
  * A token whose position is outside the table adds nothing to the weights'
  * gradients.  Both calls enqueue on `stream`; argument errors return before any
  * launch.

@@ -13,9 +13,11 @@
 // of an item's end or the item has at most eight units (or, when an eighth of the
 // work is in items of less than C / 4, at most C).  So items that divide badly among the SMs are evened out by
 // at most one cut a SM, and the splits are listed by decreasing size, which the
-// hardware then starts in that order as SMs become free.  (2,048 tokens over
-// 32,768, 256 items of 272 units on 152 SMs: 814 us with each item halved,
-// two rounds of whole items 816 us; cut this way 741 us.)
+// hardware then starts in that order as SMs become free.  (Measured on 152 SMs:
+// 2,048 tokens over 32,768, 256 items of 272 units, 740 us, uncut 826 us; a whole
+// prompt of 8,192 tokens, 512 items of 2 to 64 units, 206 us uncut and 221 us cut,
+// hence the rule for small items; ragged chunks, 292 items of 1 to 44 units, 79 us,
+// uncut 87 us.)
 //
 // Either way the split items have at most 2 ctas / heads splits in all (an item
 // of n > 1 splits has more than (n - 1) target units, or n - 1 cuts), which

@@ -113,6 +113,65 @@ def test_forward_and_gradients(cp, T, H, Hk, D, R, inter, norm, strided):
         assert (a is None and b is None) or torch.equal(a, b)
 
 
+def _whole(x, w, rows, R, inter, eps):
+    """The oracle's forward on whole arrays, float64 on the device; also the size of
+    its terms."""
+    x = x.double()
+    n = x if w is None else x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * w.double()
+    c, s = rows.double()[:, None].chunk(2, -1)
+    a = slice(0, R, 2) if inter else slice(0, R // 2)
+    b = slice(1, R, 2) if inter else slice(R // 2, R)
+    y, size = n.clone(), n.abs()
+    y[..., a], y[..., b] = n[..., a] * c - n[..., b] * s, n[..., b] * c + n[..., a] * s
+    size[..., a] = (n[..., a] * c).abs() + (n[..., b] * s).abs()
+    size[..., b] = (n[..., b] * c).abs() + (n[..., a] * s).abs()
+    return y, size
+
+
+def test_whole_arrays_are_the_oracle(cp):
+    for inter in (False, True):
+        x, w = normal(5, 3, 64, seed=1), normal(64, seed=2)
+        rows = table(9, 32)[torch.tensor([8, 0, 3, 5, 1])]
+        y, size = _whole(x, w, rows, 32, inter, 1e-5)
+        ref, rs = on.forward(f64(x), f64(w), rows.numpy(), 64, inter, 1e-5)
+        assert np.allclose(f64(y), ref, rtol=1e-13) and np.allclose(f64(size), rs, rtol=1e-13)
+
+
+@pytest.mark.parametrize("T,H,Hk,D,inter", [
+    (7400, 15, 13, 128, False),   # runs of eight heads that end inside a batch
+    (7400, 16, 16, 128, True),
+    (3701, 16, 14, 128, False),   # forward in runs of four
+    (15001, 15, 3, 64, True),
+])
+def test_many_tokens(cp, T, H, Hk, D, inter):
+    """Sizes that take the longer runs of heads, against float64 autograd of the
+    same definition.  A weight's gradient adds its T * heads terms along chains of
+    at most T * heads / lane groups + 64 < 2^9 additions: 2^-15 + 2^-18 of their
+    magnitudes, so 2^-14 size holds with room; magnitudes as in the oracle."""
+    R = D // 2
+    q, k, pos, tab, wq, wk = _inputs(T, H, Hk, D, R, True, True, seed=T)
+    dpos, dtab, dwq_, dwk_ = _cuda(pos, tab, wq, wk)
+    kw = dict(q_weight=dwq_, k_weight=dwk_, eps=1e-5, interleaved=inter)
+    qo, ko = cp.qk_norm_rope(q, k, dpos, dtab, **kw)
+    gq, gk = normal(T, H, D, seed=9).cuda(), normal(T, Hk, D, seed=10).cuda()
+    dq, dk, dwq, dwk = cp.qk_norm_rope_bwd(gq, gk, q, k, dpos, dtab, **kw)
+    rows = dtab[dpos.long()]
+    for x, w, y, g, dx, dw in ((q, dwq_, qo, gq, dq, dwq), (k, dwk_, ko, gk, dk, dwk)):
+        x64 = x.double().requires_grad_()
+        w64 = w.double().requires_grad_()
+        ref, size = _whole(x64, w64, rows, R, inter, 1e-5)
+        rdx, rdw = torch.autograd.grad(ref, (x64, w64), g.double())
+        x64, w64, ref, size = (t.detach() for t in (x64, w64, ref, size))
+        assert ((y.double() - ref).abs() <= 2 ** -8 * ref.abs() + 2 ** -18 * size).all()
+        # The magnitudes of the gradient's terms: |g| turned by |cos|, |sin|.
+        gs = _whole(g, None, torch.cat([rows[:, :R // 2], -rows[:, R // 2:]], 1), R, inter, 0)[1]
+        r = (x64.pow(2).mean(-1, keepdim=True) + 1e-5).rsqrt()
+        u, hat = gs * w64.abs(), (x64 * r).abs()
+        sx = r * (u + hat * (u * hat).mean(-1, keepdim=True))
+        assert ((dx.double() - rdx).abs() <= 2 ** -8 * rdx.abs() + 2 ** -17 * sx).all()
+        assert ((dw.double() - rdw).abs() <= 2 ** -14 * (gs * hat).sum((0, 1))).all()
+
+
 def test_in_place_and_given_outputs(cp):
     """Outputs over the inputs, inside one projection's buffer: the values
     between and behind them stay."""

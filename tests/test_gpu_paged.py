@@ -114,6 +114,10 @@ def test_attention(cp, new, kv, H, Hk, D, size, causal):
     ([1], [9000], 4, 1, 64, 64, 1.0),                    # many splits of one token
     ([1, 1], [6000, 33], 2, 2, 128, 16, 2.5),            # scores over many powers of two
     ([2, 70], [3100, 5000], 4, 2, 128, 32, 2.0),         # splits beside whole items
+    ([5, 3], [4000, 700], 10, 2, 64, 32, 1.0),           # up to 32 rows in splits
+    ([4], [5000], 16, 2, 128, 16, 1.0),
+    ([5], [20000], 5, 1, 64, 64, 1.0),                   # more splits than a round of the merge
+    ([100, 60], [2600, 2000], 4, 4, 64, 16, 2.0),        # tiles cut at several places
 ])
 def test_long_caches(cp, new, kv, H, Hk, D, size, std):
     x = Batch(new, kv, H, Hk, D, size, seed=3, std=std)
@@ -136,6 +140,31 @@ def test_many_sequences(cp):
     x.check(out, lse)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_blocks(cp, D):
+    """More blocks of tiles than the schedule kernel has threads, most of one key
+    tile, and one long cache that is cut: the blocks are listed by size over
+    several rounds."""
+    new, kv = [40] * 180 + [7], [60] * 180 + [3500]
+    x = Batch(new, kv, 33, 1, D, 64, seed=17)
+    args = x.on_gpu()
+    out, lse = cp.paged_attn(*args, **x.bounds())
+    again = cp.paged_attn(*args, **x.bounds())
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    # A few of the equal sequences and the long one against the oracle.
+    ref, rl, size, span = op.attention(
+        f64(x.q[-47:]), f64(x.kc), f64(x.vc), x.table[-2:], [0, 40, 47], kv[-2:], x.scale)
+    e = D * 2.0 ** -24 * span + 2.0 ** -18
+    check(out[-47:], ref, 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[..., None]) * size, "O")
+    assert np.all(np.abs(f64(lse[-47:]) - rl) <= e + 2.0 ** -22 * np.abs(rl))
+    # And every sequence by itself (another schedule, no cuts for the short ones).
+    q, kc, vc, t, cu, kvl = args
+    for b in (0, 1, 90, 179):
+        one, _ = cp.paged_attn(q[40 * b:40 * b + 40], kc, vc, t[b:b + 1], cu[:2], kvl[b:b + 1],
+                               max_seqlen=40, max_kv_len=60)
+        assert torch.equal(one, out[40 * b:40 * b + 40])
+
+
 def test_padded_batch_and_larger_bounds(cp):
     """Rows behind the last sequence stay, and bounds above the lengths (a
     captured program's) choose other kernels and splits for the same answer."""
@@ -153,8 +182,16 @@ def test_caches_inside_a_larger_tensor(cp):
     x = Batch([2, 1], [70, 33], 4, 2, 64, 32, seed=7)
     q, kc, vc, t, cu, kv = x.on_gpu()
     both = torch.stack([kc, vc], 1)
-    out, lse = cp.paged_attn(q, both[:, 0], both[:, 1], t, cu, kv, **x.bounds())
-    x.check(out, lse)
+    for bound in (2, 9, 200):
+        out, lse = cp.paged_attn(q, both[:, 0], both[:, 1], t, cu, kv, max_seqlen=bound,
+                                 max_kv_len=70)
+        x.check(out, lse)
+    k, v = normal(3, 2, 64, seed=1).cuda(), normal(3, 2, 64, seed=2).cuda()
+    want = both.clone()
+    cp.paged_append(k, v, both[:, 0], both[:, 1], t, cu, kv)
+    for (i, _, _, pg, row) in op.places(x.cu, x.kv, x.table, 32):
+        want[pg, 0, row], want[pg, 1, row] = k[i], v[i]
+    assert torch.equal(both.nan_to_num(9), want.nan_to_num(9))
     y = Batch([1], [9], 4, 2, 64, 32, seed=8)
     q, kc, vc, t, cu, kv = y.on_gpu()
     page = int(y.table[0, 0])
@@ -242,6 +279,32 @@ def test_append(cp, new, kv, H, Hk, D, size, R, inter, norm, with_q):
         ref, s = on.forward(f64(q)[tok], w64[0], rows, D, inter, 1e-5)
         check(qo[tok], ref, 2 ** -8 * np.abs(ref) + 2 ** -18 * s, "q")
         assert (qo[x.cu[-1]:] == 7).all()
+
+
+def test_append_of_many_tokens(cp):
+    """A size that takes the longer runs of heads: the bits of qk_norm_rope and of
+    the values."""
+    H, Hk, D, size, new = 16, 8, 128, 64, [3000, 1, 4500]
+    kv = [3100, 900, 4500]
+    x = Batch(new, kv, 1, 1, 64, size, seed=18, spoil=False)
+    _, _, _, t, cu, kvl = x.on_gpu()
+    pages = x.kc.shape[0]
+    kc, vc = (torch.zeros(pages, size, Hk, D, dtype=torch.bfloat16, device="cuda")
+              for _ in range(2))
+    qkv = normal(x.T, H + 2 * Hk, D, seed=2, std=1.5).cuda()
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    w = (1 + 0.3 * normal(D, seed=3).float()).to(torch.bfloat16).cuda()
+    tab = table(4500, 128).cuda()
+    qo = cp.paged_append(k, v, kc, vc, t, cu, kvl, rope_table=tab, k_weight=w, q=q, q_weight=w)
+    at = op.places(x.cu, kv, x.table, size)
+    pos = torch.tensor([a[2] for a in at], dtype=torch.int32, device="cuda")
+    rq, rk = cp.qk_norm_rope(q, k, pos, tab, q_weight=w, k_weight=w)
+    page = torch.tensor([a[3] for a in at], device="cuda")
+    row = torch.tensor([a[4] for a in at], device="cuda")
+    assert torch.equal(qo, rq) and torch.equal(kc[page, row], rk) and torch.equal(vc[page, row], v)
+    rest = torch.ones(pages, size, dtype=torch.bool, device="cuda")
+    rest[page, row] = False
+    assert (kc[rest] == 0).all() and (vc[rest] == 0).all()
 
 
 def test_append_leaves_out_bad_tokens(cp):
@@ -355,6 +418,12 @@ def test_a_cache_past_32_bit_offsets(cp):
     t = torch.from_numpy(table_).cuda()
     out, lse = cp.paged_attn(x.q.cuda(), kc, vc, t, cu, kv, **x.bounds())
     x.check(out, lse)
+    one = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    few, _ = cp.paged_attn(x.q[[0, x.T - 1]].cuda(), kc, vc, t, one, kv, max_seqlen=1,
+                           max_kv_len=600)
+    # The same two rows by the other kernel: each within 2^-8 (2 |O| + size) of the
+    # exact value, |v| <= 6.
+    assert (few.float() - out[[0, x.T - 1]].float()).abs().max() <= 2 * 2 ** -8 * 3 * 6
     k, v = normal(x.T, Hk, D, seed=1).cuda(), normal(x.T, Hk, D, seed=2).cuda()
     cp.paged_append(k, v, kc, vc, t, cu, kv)
     for (i, _, _, page, row) in op.places(x.cu, x.kv, table_, size)[::37]:
