@@ -67,9 +67,11 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   const int Hk = p.num_kv_heads, G = p.group;
   const int e = static_cast<int>(blockIdx.x) / Hk;
   const int h = static_cast<int>(blockIdx.x) - e * Hk;
-  if (e >= __ldcg(&p.hdr->n_items)) return;
+  // In flight together: the list has room for every CTA of the grid.
+  const int n_work = __ldcg(&p.hdr->n_items);
   const int4* wp = reinterpret_cast<const int4*>(p.work + e);
   const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1), w2 = __ldcg(wp + 2);
+  if (e >= n_work) return;
   const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
   const int blk = w1.x, kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
   // Rows of this block: [row0, row0 + kRows), those below 0 are not there.
@@ -128,10 +130,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int j = 0; j < C::kStages - 1; ++j) copy(j);
-
-  // Q as left operands: lane l holds rows l / 4 and l / 4 + 8, columns
+  // Q (in flight with the first page numbers) as left operands: lane l holds rows l / 4 and l / 4 + 8, columns
   // 2 (l % 4) + {0, 1} and + 8 of each 16 x 16 block.
   uint32_t qa[MT][D / 16][4];
   int lim[MT][2];  // keys below it are visible
@@ -152,6 +151,9 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
         qa[mt][kk][hf + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8)) : 0u;
       }
     }
+#pragma unroll
+  for (int j = 0; j < C::kStages - 1; ++j) copy(j);
+
   // Groups ending at or below this key need no mask (rows are in order, so
   // the block's first row sees the fewest keys).
   const int first_tok = max(row0, 0) / G;

@@ -98,16 +98,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TileCfg<D>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_work = __ldcg(&p.hdr->n_items);
-  if (static_cast<int>(blockIdx.x) >= n_work * p.num_kv_heads) return;
-  // After one CTA gave up on a wait, the rest of the grid does no work.
-  if (__ldcg(&p.hdr->error) == kErrTimeoutT) return;
   // The heads of a split run together; a head's blocks walk its keys in step,
-  // so most of them come from L2.
+  // so most of them come from L2.  The loads are in flight together: the list has
+  // room for every CTA of the grid.
   const int e = static_cast<int>(blockIdx.x) / p.num_kv_heads;
   const int h = static_cast<int>(blockIdx.x) - e * p.num_kv_heads;
+  const int n_work = __ldcg(&p.hdr->n_items);
+  const int err0 = __ldcg(&p.hdr->error);
   const int4* wp = reinterpret_cast<const int4*>(p.work + e);
   const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1);
+  // After one CTA gave up on a wait, the rest of the grid does no work.
+  if (e >= n_work || err0 == kErrTimeoutT) return;
   const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
   const int kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
   const int G = p.group;
