@@ -30,7 +30,7 @@ BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["plan.cpp", "api.cu", "schedule.cu", "merge.cu", "attn_fwd.cu", "attn_bwd.cu",
            "dcp.cu", "decode.cu", "noalloc.cu", "ulysses.cu", "norm_rope.cu", "paged_sched.cu",
            "paged_rows.cu", "paged_tile.cu", "serve_api.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", "work.cuh", "debug.cuh"]
+HEADERS = ["kernels.h", "ptx.cuh", "work.cuh", "debug.cuh", "paged_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -273,7 +273,7 @@ struct alignas(16) PagedMerge {
 };
 
 struct PagedLayout {
-  size_t first_off, work_off, merge_off, arrived_off, o_off, lse_off, total;
+  size_t first_off, work_off, merge_off, arrived_off, error_off, o_off, lse_off, total;
   int64_t max_work;   // splits of one KV head
   int64_t max_slots;  // slots of one KV head
 };
@@ -283,11 +283,12 @@ struct PagedShape {
   bool tiles;      // the tensor-memory kernel (else the register kernel)
   int rows;        // rows of a block
   int unit;        // keys of a unit
-  int min_units;   // a split is not made for less than so many units
+  int min_units;   // tiles, and few rows of many items: a split has at least so many units
   int whole;       // items of up to so many units stay whole
   int ctas;        // a split does at least 1 / ctas of the whole work
   int round;       // CTAs resident at once (at most ctas)
   bool join;       // the last CTA of a split item joins it (else a merge kernel)
+  bool plan;       // no schedule kernel: every warp works the list out (paged_plan.cuh)
 };
 
 struct PagedParams {
@@ -304,12 +305,28 @@ struct PagedParams {
   int* first;         // [num_seqs + 1]: first item of each sequence
   PagedWork* work;    // [max_work]
   PagedMerge* merge;  // [max_slots / 2]
-  int* arrived;       // [max_slots / 2, num_kv_heads]: splits that are done (register kernel)
+  int* arrived;       // [max_slots / 2, num_kv_heads]: splits that are done (join)
+  int* cta_error;     // [max_work, num_kv_heads]: bad pages seen (plan)
   float* o_part;      // [max_slots, num_kv_heads, rows, D], normalised
   float* lse_part;    // [max_slots, num_kv_heads, rows], natural log
   long long max_work, max_slots;
   PagedShape shape;
 };
+
+// Units of a split when there are few rows: with few items the splits are made to
+// fit one round of resident CTAs (sum of ceil(u / target) <= all / target + items),
+// else to be several rounds that even out, of at least min_units: a join costs as
+// much as about 20 units (with 4, 24 and 32: 65 caches of 327 to 655 keys, 4 heads,
+// 27.0, 18.5 and 18.4 us; 90 of 601 to 4,808 keys, 2 heads, 60.8, 59.4 and 64.6).
+__device__ __forceinline__ int paged_rows_target(const PagedShape& s, long long all, int items,
+                                                 int heads) {
+  const long long lanes = static_cast<long long>(items) * heads;
+  const bool one = 2 * lanes <= s.round;
+  const long long share = one ? s.round - lanes : s.ctas;
+  const long long target = (all * heads + share - 1) / share;
+  const long long least = one ? 1 : s.min_units;
+  return static_cast<int>(target < least ? least : (target > (1 << 30) ? (1 << 30) : target));
+}
 
 cudaError_t launch_paged_schedule(const PagedParams& p, cudaStream_t stream);
 cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream);

@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include "kernels.h"
+#include "paged_plan.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -52,7 +53,7 @@ __device__ __forceinline__ int at(int r, int c) {
 
 }  // namespace
 
-template <int D, int MT>
+template <int D, int MT, bool PLAN>
 __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedParams p) {
   using C = RowsCfg<D>;
   constexpr int kRows = 16 * MT;
@@ -63,23 +64,42 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   __shared__ int s_last;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int Hk = p.num_kv_heads, G = p.group;
   const int e = static_cast<int>(blockIdx.x) / Hk;
   const int h = static_cast<int>(blockIdx.x) - e * Hk;
-  // In flight together: the list has room for every CTA of the grid.
-  const int n_work = __ldcg(&p.hdr->n_items);
-  const int4* wp = reinterpret_cast<const int4*>(p.work + e);
-  const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1), w2 = __ldcg(wp + 2);
-  if (e >= n_work) return;
-  const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
-  const int blk = w1.x, kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  PagedWork w;
+  if (PLAN) {
+    const PagedPlan plan = make_plan(p, lane);
+    if (e >= plan.splits) return;
+    w = plan_split(p, plan, e);
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // In flight together: the list has room for every CTA of the grid.
+    const int n_work = __ldcg(&p.hdr->n_items);
+    const int4* wp = reinterpret_cast<const int4*>(p.work + e);
+    const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1), w2 = __ldcg(wp + 2);
+    if (e >= n_work) return;
+    w.tok0 = w0.x;
+    w.q_len = w0.y;
+    w.kv_len = w0.z;
+    w.seq = w0.w;
+    w.blk = w1.x;
+    w.kv_lo = w1.y;
+    w.kv_hi = w1.z;
+    w.slot = w1.w;
+    w.slot0 = w2.x;
+    w.n = w2.y;
+    w.item = w2.z;
+  }
+  const int tok0 = w.tok0, q_len = w.q_len, kv_len = w.kv_len, seq = w.seq;
+  const int blk = w.blk, kv_lo = w.kv_lo, kv_hi = w.kv_hi, slot = w.slot;
   // Rows of this block: [row0, row0 + kRows), those below 0 are not there.
   const int all_rows = q_len * G;
   const int n_blk = (all_rows + kRows - 1) / kRows;
   const int row0 = all_rows - (n_blk - blk) * kRows;
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool bad_page = false;
   const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;
   const int page_mask = (1 << p.page_shift) - 1;
   const size_t row_pitch = static_cast<size_t>(Hk) * D;
@@ -105,7 +125,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
         if (j + NG < n) next_page[g] = __ldg(pages + (group_key(j + NG) >> p.page_shift));
         int last = j < n ? kv_len : 0;  // keys at or beyond it are filled with zeros
         if (page < 0 || page >= p.num_pages) {
-          if (lane == 0 && j < n) atomicCAS(&p.hdr->error, 0, 1);  // CPATTN_ERR_INVALID_ARG
+          bad_page = bad_page || j < n;
           page = 0;
           last = 0;
         }
@@ -280,7 +300,11 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
 
   // Join the warps' states (their rings are done with) and write the rows.
   cp_async_wait<0>();
-  __syncthreads();
+  const bool any_bad = __syncthreads_or(bad_page);
+  if (threadIdx.x == 0) {
+    if (PLAN) p.cta_error[blockIdx.x] = any_bad ? 1 : 0;
+    else if (any_bad) atomicCAS(&p.hdr->error, 0, 1);  // CPATTN_ERR_INVALID_ARG
+  }
   float* so = reinterpret_cast<float*>(smem) + warp * kRows * D;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -344,20 +368,20 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
     }
   };
   join(slot);
-  if (slot < 0 || MT > 1) return;  // 32 rows: see paged_merge_kernel
+  if (slot < 0 || PLAN || MT > 1) return;  // else paged_merge_kernel joins them
 
   // The last of an item's splits to be done joins them all, in their order:
   // each warp takes every fourth split, with its own running maximum.
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    s_last = atomicAdd(p.arrived + static_cast<size_t>(w2.z) * Hk + h, 1) == w2.y - 1;
+    s_last = atomicAdd(p.arrived + static_cast<size_t>(w.item) * Hk + h, 1) == w.n - 1;
     __threadfence();
   }
   __syncthreads();
   if (!s_last) return;
-  const int splits = w2.y;
-  const size_t part0 = (static_cast<size_t>(w2.x) * Hk + h) * kRows;
+  const int splits = w.n;
+  const size_t part0 = (static_cast<size_t>(w.slot0) * Hk + h) * kRows;
   const size_t pitch = static_cast<size_t>(Hk) * kRows;  // rows from split to split
   constexpr int kPer = D / 32;                          // floats of a row each lane owns
   constexpr int kAhead = 4;                             // splits in flight of each of
@@ -436,9 +460,9 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   join(-1);
 }
 
-template <int D, int MT>
+template <int D, int MT, bool PLAN>
 static cudaError_t launch_paged_rows_t(const PagedParams& p, cudaStream_t stream) {
-  auto kern = paged_rows_kernel<D, MT>;
+  auto kern = paged_rows_kernel<D, MT, PLAN>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              RowsCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
@@ -451,14 +475,21 @@ static cudaError_t launch_paged_rows_t(const PagedParams& p, cudaStream_t stream
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = PLAN ? 0 : 1;  // after the schedule kernel
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream) {
+template <int D>
+static cudaError_t launch_paged_rows_d(const PagedParams& p, cudaStream_t stream) {
   if (p.shape.rows == 16)
-    return D == 64 ? launch_paged_rows_t<64, 1>(p, stream) : launch_paged_rows_t<128, 1>(p, stream);
-  return D == 64 ? launch_paged_rows_t<64, 2>(p, stream) : launch_paged_rows_t<128, 2>(p, stream);
+    return p.shape.plan ? launch_paged_rows_t<D, 1, true>(p, stream)
+                        : launch_paged_rows_t<D, 1, false>(p, stream);
+  return p.shape.plan ? launch_paged_rows_t<D, 2, true>(p, stream)
+                      : launch_paged_rows_t<D, 2, false>(p, stream);
+}
+
+cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream) {
+  return D == 64 ? launch_paged_rows_d<64>(p, stream) : launch_paged_rows_d<128>(p, stream);
 }
 
 }  // namespace cpattn

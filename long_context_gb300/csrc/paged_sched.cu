@@ -5,7 +5,7 @@
 // all items of one KV head; every KV head is cut alike.
 //
 // Few rows (HBM bound; two CTAs a SM): an item of u units becomes
-// ceil(u / target) equal splits, target = max(min_units, ceil(W heads / ctas)).
+// ceil(u / target) equal splits (see paged_rows_target).
 //
 // Tiles (one CTA a SM, an item is up to hundreds of units): the items' units are
 // laid end to end and cut at every multiple of one SM's share
@@ -28,6 +28,7 @@
 // The merge joins an item's normalised partials: LSE = ln sum exp(lse_s),
 // O = sum exp(lse_s - LSE) O_s.
 #include "kernels.h"
+#include "paged_plan.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -98,105 +99,7 @@ __device__ __forceinline__ int item_units(const PagedParams& p, const PagedItem&
 
 }  // namespace
 
-// Up to 32 sequences of one block of few rows each (a small decoding step): every
-// warp works out all splits in its lanes, without a barrier, and the warps share
-// the writing.
-__global__ void __launch_bounds__(128) paged_schedule_small_kernel(const PagedParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int B = p.num_seqs;
-  int lo = 0, hi = 0, kv = 0;
-  if (lane < B) {
-    lo = p.cu_seqlens[lane];
-    hi = p.cu_seqlens[lane + 1];
-    kv = p.kv_lens[lane];
-  }
-  const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
-  const bool bad = lo < 0 || hi < lo || hi > p.total_q || hi - lo > p.max_seqlen || kv < 0 ||
-                   kv > p.max_kv_len || kv > cap || (lane == 0 && lo != 0);
-  if (__any_sync(0xffffffffu, bad)) {
-    if (threadIdx.x == 0) {
-      p.hdr->error = 1;  // CPATTN_ERR_INVALID_ARG
-      p.hdr->n_items = 0;
-      p.hdr->pad[0] = 0;
-    }
-    return;
-  }
-  const bool have = lane < B && hi > lo;
-  const int units = have ? (kv + p.shape.unit - 1) / p.shape.unit : 0;
-  const unsigned with = __ballot_sync(0xffffffffu, have);
-  long long all = units;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const int lanes = __popc(with) * p.num_kv_heads;
-  const int share = 2 * lanes <= p.shape.round ? p.shape.round - lanes : p.shape.ctas;
-  long long target = (all * p.num_kv_heads + share - 1) / share;
-  if (target < p.shape.min_units) target = p.shape.min_units;
-  int n = have ? 1 : 0, per = units;
-  if (units > target) {
-    n = static_cast<int>((units + target - 1) / target);
-    per = (units + n - 1) / n;
-    n = (units + per - 1) / per;
-  }
-  // First split, slot and number among the split items, in one scan.
-  const long long mine = n + (n > 1 ? (static_cast<long long>(n) << 32) + (1ll << 48) : 0);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const long long total = __shfl_sync(0xffffffffu, incl, 31);
-  const long long before = incl - mine;
-  const int base = static_cast<int>(before & 0xffffffffll);
-  const int slot = n > 1 ? static_cast<int>((before >> 32) & 0xffff) : -1;
-  const int item = static_cast<int>(before >> 48);
-  const int splits = static_cast<int>(total & 0xffffffffll);
-  const int merges = static_cast<int>(total >> 48);
-  for (int e0 = threadIdx.x - lane; e0 < splits; e0 += 128) {
-    const int e = e0 + lane;
-    // The last lane whose first split is at most e (a lane without splits begins
-    // where the next one with some does, and behind the last at `splits`).
-    int b = 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      if (__shfl_sync(0xffffffffu, base, b + o) <= e) b += o;
-    PagedWork w;
-    w.tok0 = __shfl_sync(0xffffffffu, lo, b);
-    w.q_len = __shfl_sync(0xffffffffu, hi, b) - w.tok0;
-    w.kv_len = __shfl_sync(0xffffffffu, kv, b);
-    w.seq = b;
-    w.blk = 0;
-    const int s = e - __shfl_sync(0xffffffffu, base, b);
-    const int step = __shfl_sync(0xffffffffu, per, b);
-    w.kv_lo = s * step * p.shape.unit;
-    w.kv_hi = min(w.kv_len, (s + 1) * step * p.shape.unit);
-    w.slot0 = __shfl_sync(0xffffffffu, slot, b);
-    w.slot = w.slot0 < 0 ? -1 : w.slot0 + s;
-    w.n = __shfl_sync(0xffffffffu, n, b);
-    w.item = __shfl_sync(0xffffffffu, item, b);
-    w.pad = 0;
-    if (e < splits) p.work[e] = w;
-  }
-  if (p.shape.join) {
-    for (int i = threadIdx.x; i < merges * p.num_kv_heads; i += 128) p.arrived[i] = 0;
-  } else if (threadIdx.x < 32 && n > 1) {
-    PagedMerge m = {};
-    m.tok0 = lo;
-    m.q_len = hi - lo;
-    m.blk = 0;
-    m.slot0 = slot;
-    m.n = n;
-    p.merge[item] = m;
-  }
-  if (threadIdx.x == 0) {
-    p.hdr->error = 0;
-    p.hdr->n_items = splits;
-    p.hdr->pad[0] = merges;
-  }
-}
-
-// NT threads; batches of up to 128 items take 128, whose barriers are quicker.
+// NT threads: few for small batches, whose barriers are then quicker.
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p) {
   constexpr int kPsThreads = NT;
@@ -257,15 +160,14 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   }
   ps_scan<NT>(sum, warp_sums);
   const long long all = warp_sums[NT / 32 - 1];
-  // Few rows, few items: the splits are made to fit one round of resident CTAs
-  // (sum of ceil(u / target) <= all / target + items), else to be several
-  // rounds that even out.
-  const long long lanes = static_cast<long long>(items) * p.num_kv_heads;
-  const long long share =
-      !tiles && 2 * lanes <= p.shape.round ? p.shape.round - lanes : p.shape.ctas;
-  long long target_ll = (all * p.num_kv_heads + share - 1) / share;
-  if (target_ll < p.shape.min_units) target_ll = p.shape.min_units;
-  const int target = static_cast<int>(min(target_ll, 1ll << 30));
+  int target;
+  if (tiles) {
+    const long long share = (all * p.num_kv_heads + p.shape.ctas - 1) / p.shape.ctas;
+    target = static_cast<int>(
+        min(max(share, static_cast<long long>(p.shape.min_units)), 1ll << 30));
+  } else {
+    target = paged_rows_target(p.shape, all, items, p.num_kv_heads);
+  }
   const int snap = target / 16 + 1;
   // Tiles: when small items hold an eighth of the work, they even out the SMs
   // by themselves (started last), and only items above a share are cut.
@@ -407,29 +309,44 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
 }
 
 cudaError_t launch_paged_schedule(const PagedParams& p, cudaStream_t stream) {
-  if (!p.shape.tiles && p.num_seqs <= 32 &&
-      static_cast<long long>(p.max_seqlen) * p.group <= p.shape.rows)
-    paged_schedule_small_kernel<<<1, 128, 0, stream>>>(p);
-  else if (p.total_q * p.group / p.shape.rows + p.num_seqs <= 128)
-    paged_schedule_kernel<128><<<1, 128, 0, stream>>>(p);
-  else
-    paged_schedule_kernel<1024><<<1, 1024, 0, stream>>>(p);
+  // At most so many items: by the rows in all, and by the blocks of each sequence.
+  const long long rows = static_cast<long long>(p.max_seqlen) * p.group;
+  const long long items = min(p.total_q * p.group / p.shape.rows + p.num_seqs,
+                              p.num_seqs * ((rows + p.shape.rows - 1) / p.shape.rows));
+  if (items <= 128) paged_schedule_kernel<128><<<1, 128, 0, stream>>>(p);
+  else if (items <= 512) paged_schedule_kernel<512><<<1, 512, 0, stream>>>(p);
+  else paged_schedule_kernel<1024><<<1, 1024, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 // A warp joins R rows of one item and KV head at a time, S splits of each in
 // flight; lane l holds the weight of row l % R and split l / R of a round of
 // 32 / R splits.
-template <int D, int R, int S>
+template <int D, int R, int S, bool PLAN>
 __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(const PagedParams p) {
   constexpr int kPer = D / 32;  // floats of a row each lane owns
   constexpr int kRound = 32 / R;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
+  PagedPlan plan;
+  if (PLAN) plan = make_plan(p, lane);  // reads the lengths alone: beside the attention
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (PLAN && blockIdx.x == 0) {
+    // The error word of the whole call.
+    int error = 0;
+    for (int i = threadIdx.x; i < plan.splits * p.num_kv_heads; i += kPmThreads)
+      error |= __ldcg(p.cta_error + i);
+    error = __syncthreads_or(error);
+    if (threadIdx.x == 0) {
+      p.hdr->error = plan.bad || error ? 1 : 0;  // CPATTN_ERR_INVALID_ARG
+      p.hdr->n_items = plan.splits;
+      p.hdr->pad[0] = plan.merges;
+    }
+  }
   const int lr = lane % R, ls = lane / R;
   const int rows = p.shape.rows, Hk = p.num_kv_heads;
   const int groups = (rows + R - 1) / R;
-  const long long total = static_cast<long long>(__ldcg(&p.hdr->pad[0])) * Hk * groups;
+  const int merges = PLAN ? plan.merges : __ldcg(&p.hdr->pad[0]);
+  const long long total = static_cast<long long>(merges) * Hk * groups;
   const long long step = static_cast<long long>(gridDim.x) * (kPmThreads / 32);
   const long long pitch = static_cast<long long>(Hk) * rows;  // rows from split to split
   for (long long x = static_cast<long long>(blockIdx.x) * (kPmThreads / 32) + (threadIdx.x >> 5);
@@ -437,10 +354,20 @@ __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(const PagedPara
     const int r0 = static_cast<int>(x % groups) * R;
     const long long mh = x / groups;
     const int h = static_cast<int>(mh % Hk);
-    const int4* mp = reinterpret_cast<const int4*>(p.merge + mh / Hk);
-    const int4 m0 = __ldcg(mp);
-    const int n = __ldcg(mp + 1).x;
-    const int tok0 = m0.x, q_len = m0.y, blk = m0.z, slot0 = m0.w;
+    PagedMerge item;
+    if (PLAN) {
+      item = plan_merge(plan, static_cast<int>(mh / Hk));
+    } else {
+      const int4* mp = reinterpret_cast<const int4*>(p.merge + mh / Hk);
+      const int4 m0 = __ldcg(mp);
+      item.n = __ldcg(mp + 1).x;
+      item.tok0 = m0.x;
+      item.q_len = m0.y;
+      item.blk = m0.z;
+      item.slot0 = m0.w;
+    }
+    const int n = item.n, tok0 = item.tok0, q_len = item.q_len, blk = item.blk;
+    const int slot0 = item.slot0;
     const long long all_rows = static_cast<long long>(q_len) * p.group;
     const long long n_blk = (all_rows + rows - 1) / rows;
     const long long row0 = all_rows - (n_blk - blk) * rows + r0;
@@ -530,9 +457,26 @@ __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(const PagedPara
   }
 }
 
+template <int D>
+static cudaError_t launch_paged_merge_d(const PagedParams& p, const cudaLaunchConfig_t& cfg) {
+  // Tiles: many rows of few splits.  Else: few rows of many splits.
+  if (p.shape.tiles) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, 8, 1, false>, p);
+  return p.shape.plan ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, 2, 8, true>, p)
+                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, 2, 4, false>, p);
+}
+
 cudaError_t launch_paged_merge(const PagedParams& p, int D, int num_sms, cudaStream_t stream) {
+  // No more merges than items, nor than half the slots.
+  const long long blocks =
+      (static_cast<long long>(p.max_seqlen) * p.group + p.shape.rows - 1) / p.shape.rows;
+  const long long items = min(min(p.total_q * p.group / p.shape.rows + p.num_seqs,
+                                  p.num_seqs * blocks), p.max_slots / 2);
+  const int at_once = p.shape.tiles ? 8 : 2;  // rows of a warp
+  const long long warps = items * p.num_kv_heads * ((p.shape.rows + at_once - 1) / at_once);
+  long long grid = (warps + kPmThreads / 32 - 1) / (kPmThreads / 32);
+  grid = grid < 1 ? 1 : min(grid, num_sms * 4LL);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms * 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kPmThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -540,12 +484,7 @@ cudaError_t launch_paged_merge(const PagedParams& p, int D, int num_sms, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Tiles: many rows of few splits.  32 rows: many splits.
-  if (p.shape.tiles)
-    return D == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 8, 1>, p)
-                   : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 8, 1>, p);
-  return D == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 2, 4>, p)
-                 : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 2, 4>, p);
+  return D == 64 ? launch_paged_merge_d<64>(p, cfg) : launch_paged_merge_d<128>(p, cfg);
 }
 
 }  // namespace cpattn

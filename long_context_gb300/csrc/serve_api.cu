@@ -7,6 +7,7 @@
 
 #include "cpattn.h"
 #include "kernels.h"
+#include "paged_plan.cuh"
 
 namespace cpattn {
 
@@ -55,11 +56,13 @@ int page_shift_of(int32_t page_size) {
   return -1;
 }
 
-PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
+PagedShape paged_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   PagedShape s;
   const int64_t rows = group * max_seqlen;
   s.tiles = rows > 32;
-  s.join = rows <= 16;
+  // A sequence's rows are one block, a lane's to plan.
+  s.plan = !s.tiles && num_seqs <= kPlanSeqs;
+  s.join = rows <= 16 && !s.plan;
   if (s.tiles) {
     s.rows = kNQ * static_cast<int>(kBM / group * group);
     s.unit = kBN;
@@ -72,7 +75,8 @@ PagedShape paged_shape(int64_t group, int32_t max_seqlen) {
   } else {
     s.rows = rows <= 16 ? 16 : 32;
     s.unit = 64;
-    s.min_units = s.whole = 1;
+    s.min_units = 24;
+    s.whole = 1;
     s.ctas = 608;
     s.round = 304;
   }
@@ -119,6 +123,8 @@ PagedLayout paged_layout(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int3
   off = serve_align(off + sizeof(PagedMerge) * static_cast<size_t>(l.max_slots / 2 + 1));
   l.arrived_off = off;
   off = serve_align(off + sizeof(int) * static_cast<size_t>(l.max_slots / 2 + 1) * Hk);
+  l.error_off = off;
+  if (s.plan) off = serve_align(off + sizeof(int) * static_cast<size_t>(l.max_work) * Hk);
   const size_t rows = static_cast<size_t>(l.max_slots) * Hk * s.rows;
   l.o_off = off;
   off = serve_align(off + rows * D * sizeof(float));
@@ -355,7 +361,7 @@ extern "C" size_t cpattn_paged_attn_workspace_size(int64_t total_q, int32_t num_
       (head_dim != 64 && head_dim != 128) || num_heads / num_kv_heads > kPagedMaxGroup)
     return 0;
   return paged_layout(total_q, num_seqs, num_heads, num_kv_heads, head_dim,
-                      paged_shape(num_heads / num_kv_heads, max_seqlen))
+                      paged_shape(num_heads / num_kv_heads, max_seqlen, num_seqs))
       .total;
 }
 
@@ -397,7 +403,7 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   if (lse != nullptr && !aligned(lse, 4)) return CPATTN_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, kServeAlign)) return CPATTN_ERR_INVALID_ARG;
   PagedParams p{};
-  p.shape = paged_shape(group, max_seqlen);
+  p.shape = paged_shape(group, max_seqlen, num_seqs);
   const PagedLayout lay =
       paged_layout(total_q, num_seqs, num_heads, num_kv_heads, head_dim, p.shape);
   if (workspace_bytes < lay.total) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
@@ -432,12 +438,25 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   p.work = reinterpret_cast<PagedWork*>(ws + lay.work_off);
   p.merge = reinterpret_cast<PagedMerge*>(ws + lay.merge_off);
   p.arrived = reinterpret_cast<int*>(ws + lay.arrived_off);
+  p.cta_error = reinterpret_cast<int*>(ws + lay.error_off);
   p.o_part = reinterpret_cast<float*>(ws + lay.o_off);
   p.lse_part = reinterpret_cast<float*>(ws + lay.lse_off);
+  // The grid: no more splits than units, nor (a plan's items are at most num_seqs)
+  // than one round when they are made to fit one.  CTAs without work cost a small
+  // step a round of their own.
   p.max_work = lay.max_work;
+  const int64_t units = (static_cast<int64_t>(max_kv_len) + p.shape.unit - 1) / p.shape.unit;
+  const int64_t items = total_q * group / p.shape.rows + num_seqs;
+  if (units < 1) p.max_work = p.max_work < items ? p.max_work : items;
+  else if (p.max_work / units >= items) p.max_work = items * units;
+  const int64_t lanes = static_cast<int64_t>(num_seqs) * num_kv_heads;
+  if (p.shape.plan && 2 * lanes <= p.shape.round && p.max_work > p.shape.round / num_kv_heads)
+    p.max_work = p.shape.round / num_kv_heads;
   p.max_slots = lay.max_slots;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_paged_schedule(p, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+  // Without rows there is still the error word to write.
+  if ((!p.shape.plan || !any) && launch_paged_schedule(p, s) != cudaSuccess)
+    return CPATTN_ERR_CUDA;
   if (!any) return CPATTN_OK;
   if (p.shape.tiles) {
     CUtensorMap tq, tk, tv, to;
@@ -450,8 +469,8 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   } else if (launch_paged_rows(p, head_dim, s) != cudaSuccess) {
     return CPATTN_ERR_CUDA;
   }
-  // Short items are never split.
-  if (!p.shape.join && max_kv_len > p.shape.whole * p.shape.unit &&
+  // Short items are never split; after a plan the merge also writes the error word.
+  if (!p.shape.join && (p.shape.plan || max_kv_len > p.shape.whole * p.shape.unit) &&
       launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   return CPATTN_OK;
