@@ -218,6 +218,7 @@ struct NormRopeParams {
   int rot, max_pos, q_heads, kv_heads;
   long long total_tokens;
   float eps;
+  float sign;  // of the rotation: 1, or -1 for its inverse
   int* status;
   const int *cu_seqlens, *kv_lens, *page_table;
   int num_seqs, num_pages, page_shift, max_pages;

@@ -10,6 +10,7 @@
 // position p holds cos of the R/2 angles, then sin.  Gradients, with
 // hat = x r: g is dy rotated back (sin negated), and
 //   dw = sum over rows of g hat,  u = g w,  dx = r (u - hat mean(u hat)).
+// Without weights dx is g: the forward kernel with its sine negated.
 //
 // HBM bound: a row is read once and written once (the backward reads two rows
 // and writes one).  D / 8 lanes own a row.  The rows reach shared memory by
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kNrThreads, PAGED ? 4 : 5) norm_rope_kernel(co
   const bool plain = PAGED && which == 2;  // values are copied as they are
   place_lane(t, c, turning ? p.rot : 0, INTERLEAVED);
   load_turn<INTERLEAVED>(t, p.table + static_cast<size_t>(ok ? pos : 0) * p.rot, p.rot, c,
-                         ok && !plain, 1.f);
+                         ok && !plain, p.sign);
   // The weights go into the rotation's coefficients: with n = x r w,
   // y = r (x (w cos) + x' (w' sin)).
   const __nv_bfloat16* wp = which == 0 ? p.q_weight : p.k_weight;
@@ -297,18 +298,15 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
   const long long x_stride = is_k ? p.k_stride : p.q_stride;
   const long long g_stride = is_k ? p.dk_out_stride : p.dq_out_stride;
   const long long o_stride = is_k ? p.dk_stride : p.dq_stride;
-  const bool normed = p.q_weight != nullptr;
   const bool turning = p.table != nullptr;
   Turn t;
   place_lane(t, c, turning ? p.rot : 0, INTERLEAVED);
   float2 wa[2], wb[2], dwa[2], dwb[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) wa[i] = wb[i] = dwa[i] = dwb[i] = both2(0.f);
-  if (normed) {
-    const __nv_bfloat16* wp = is_k ? p.k_weight : p.q_weight;
-    unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.lo)), wa);
-    unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.hi)), wb);
-  }
+  for (int i = 0; i < 2; ++i) dwa[i] = dwb[i] = both2(0.f);
+  const __nv_bfloat16* wp = is_k ? p.k_weight : p.q_weight;
+  unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.lo)), wa);
+  unpack4(__ldg(reinterpret_cast<const uint2*>(wp + t.hi)), wb);
   const long long stride = static_cast<long long>(ctas) * kGroups;
   // The next batch's rows (of this unit or the next) are copied to shared memory
   // while the current one's are used; a unit's batches share its angles.  Whole
@@ -335,9 +333,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
       const uint32_t dst = mine + (buf * 2 * UNIT + u) * (kNrThreads * 16);
       if (h < a.end) {
         cp_async16(dst, gin + a.token * g_stride + h * D + c * 8, 16);
-        if (normed)
-          cp_async16(dst + UNIT * (kNrThreads * 16), xin + a.token * x_stride + h * D + c * 8,
-                     16);
+        cp_async16(dst + UNIT * (kNrThreads * 16), xin + a.token * x_stride + h * D + c * 8, 16);
       }
     }
     cp_async_commit();
@@ -372,34 +368,32 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
         unpack4(*reinterpret_cast<const uint2*>(piece + t.lo * 2), a);
         unpack4(*reinterpret_cast<const uint2*>(piece + t.hi * 2), b);
         apply_turn<INTERLEAVED>(t, a, b);  // g
-        if (normed) {
-          const uint8_t* px = piece + UNIT * (kNrThreads * 16);
-          float2 xa[2], xb[2];
-          unpack4(*reinterpret_cast<const uint2*>(px + t.lo * 2), xa);
-          unpack4(*reinterpret_cast<const uint2*>(px + t.hi * 2), xb);
-          float2 ss = both2(0.f), dot = both2(0.f);
+        const uint8_t* px = piece + UNIT * (kNrThreads * 16);
+        float2 xa[2], xb[2];
+        unpack4(*reinterpret_cast<const uint2*>(px + t.lo * 2), xa);
+        unpack4(*reinterpret_cast<const uint2*>(px + t.hi * 2), xb);
+        float2 ss = both2(0.f), dot = both2(0.f);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            ss = __ffma2_rn(xa[k], xa[k], ss);
-            ss = __ffma2_rn(xb[k], xb[k], ss);
-            dot = __ffma2_rn(__fmul2_rn(a[k], wa[k]), xa[k], dot);
-            dot = __ffma2_rn(__fmul2_rn(b[k], wb[k]), xb[k], dot);
-          }
-          const float sum = row_sum<LG>(ss.x + ss.y);
-          const float prod = row_sum<LG>(dot.x + dot.y);
-          const float r = rsqrtf(sum * (1.f / D) + p.eps);
-          const float2 r2 = both2(r);
-          const float2 m2 = both2(-prod * r * (1.f / D));  // -mean(u hat)
+        for (int k = 0; k < 2; ++k) {
+          ss = __ffma2_rn(xa[k], xa[k], ss);
+          ss = __ffma2_rn(xb[k], xb[k], ss);
+          dot = __ffma2_rn(__fmul2_rn(a[k], wa[k]), xa[k], dot);
+          dot = __ffma2_rn(__fmul2_rn(b[k], wb[k]), xb[k], dot);
+        }
+        const float sum = row_sum<LG>(ss.x + ss.y);
+        const float prod = row_sum<LG>(dot.x + dot.y);
+        const float r = rsqrtf(sum * (1.f / D) + p.eps);
+        const float2 r2 = both2(r);
+        const float2 m2 = both2(-prod * r * (1.f / D));  // -mean(u hat)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 ha = __fmul2_rn(xa[k], r2), hb = __fmul2_rn(xb[k], r2);
-            if (count) {
-              dwa[k] = __ffma2_rn(a[k], ha, dwa[k]);
-              dwb[k] = __ffma2_rn(b[k], hb, dwb[k]);
-            }
-            a[k] = __fmul2_rn(__ffma2_rn(ha, m2, __fmul2_rn(a[k], wa[k])), r2);
-            b[k] = __fmul2_rn(__ffma2_rn(hb, m2, __fmul2_rn(b[k], wb[k])), r2);
+        for (int k = 0; k < 2; ++k) {
+          const float2 ha = __fmul2_rn(xa[k], r2), hb = __fmul2_rn(xb[k], r2);
+          if (count) {
+            dwa[k] = __ffma2_rn(a[k], ha, dwa[k]);
+            dwb[k] = __ffma2_rn(b[k], hb, dwb[k]);
           }
+          a[k] = __fmul2_rn(__ffma2_rn(ha, m2, __fmul2_rn(a[k], wa[k])), r2);
+          b[k] = __fmul2_rn(__ffma2_rn(hb, m2, __fmul2_rn(b[k], wb[k])), r2);
         }
         if (count) {
           __nv_bfloat16* dst = out + at.token * o_stride + h * D;
@@ -412,7 +406,6 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_bwd_kernel(const Norm
     }
     at = ahead;
   }
-  if (!normed) return;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     *reinterpret_cast<float2*>(&red[group][t.lo + 2 * k]) = dwa[k];
@@ -520,7 +513,6 @@ static cudaError_t launch_norm_rope_bwd_t(NormRopeBwdParams p, bool interleaved,
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (p.q_weight == nullptr) return cudaSuccess;
   // No tokens: both sums are empty (zero rows of partials) and come out zero.
   const bool any = p.total_tokens > 0;
   cudaLaunchConfig_t cfg = {};
@@ -538,17 +530,17 @@ static cudaError_t launch_norm_rope_bwd_t(NormRopeBwdParams p, bool interleaved,
 
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, bool interleaved, float* dqw,
                                  float* dkw, int num_sms, cudaStream_t stream) {
-  // Runs of eight heads (four batches of two) share a position's angles and the
-  // unit's bookkeeping: 16,384 tokens of 64 heads 125 us, runs of two 171 us,
-  // two batches of four 133 us.  They have to leave every lane group four units
-  // or the groups even out badly: 4,999 tokens of 20 heads 18.4 us, runs of two
-  // 16.4 us.
+  // Runs of four heads (two batches of two) share a position's angles and the
+  // unit's bookkeeping: 14,000 tokens of 40 heads of 128 73 us, runs of two 82 us
+  // (16,384 of 64 heads 126 us, runs of eight 135 us).  They have to leave every
+  // lane group three units or the groups even out badly: 4,999 tokens of 20 heads
+  // of 64 16.4 us, runs of two 14.5 us.
   const long long groups = 3LL * num_sms * (kNrThreads / (D / 8));
-  const bool many = p.total_tokens * ((p.q_heads + 7) / 8 + (p.kv_heads + 7) / 8) >= 4 * groups;
+  const bool many = p.total_tokens * ((p.q_heads + 3) / 4 + (p.kv_heads + 3) / 4) >= 3 * groups;
   if (D == 64)
-    return many ? launch_norm_rope_bwd_t<64, 2, 4>(p, interleaved, dqw, dkw, num_sms, stream)
+    return many ? launch_norm_rope_bwd_t<64, 2, 2>(p, interleaved, dqw, dkw, num_sms, stream)
                 : launch_norm_rope_bwd_t<64, 2, 1>(p, interleaved, dqw, dkw, num_sms, stream);
-  return many ? launch_norm_rope_bwd_t<128, 2, 4>(p, interleaved, dqw, dkw, num_sms, stream)
+  return many ? launch_norm_rope_bwd_t<128, 2, 2>(p, interleaved, dqw, dkw, num_sms, stream)
               : launch_norm_rope_bwd_t<128, 2, 1>(p, interleaved, dqw, dkw, num_sms, stream);
 }
 

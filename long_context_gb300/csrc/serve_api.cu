@@ -193,6 +193,7 @@ extern "C" int cpattn_qk_norm_rope(const void* q, int64_t q_stride, const void* 
   p.kv_heads = num_kv_heads;
   p.total_tokens = total_tokens;
   p.eps = eps;
+  p.sign = 1.f;
   p.status = status;
   return launch_norm_rope(p, head_dim, interleaved != 0, dev.num_sms,
                           static_cast<cudaStream_t>(stream)) ==
@@ -247,6 +248,31 @@ extern "C" int cpattn_qk_norm_rope_bwd(
   DeviceInfo dev;
   st = serve_device(&dev);
   if (st != CPATTN_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!normed) {  // the inverse rotation of the gradients
+    if (total_tokens == 0) return CPATTN_OK;
+    NormRopeParams f{};
+    f.q = static_cast<const __nv_bfloat16*>(dq_out);
+    f.k = static_cast<const __nv_bfloat16*>(dk_out);
+    f.q_out = static_cast<__nv_bfloat16*>(dq);
+    f.k_out = static_cast<__nv_bfloat16*>(dk);
+    f.q_stride = dq_out_stride;
+    f.k_stride = dk_out_stride;
+    f.q_out_stride = dq_stride;
+    f.k_out_stride = dk_stride;
+    f.positions = positions;
+    f.table = rope_table;
+    f.rot = rotary_dim;
+    f.max_pos = max_position;
+    f.q_heads = num_heads;
+    f.kv_heads = num_kv_heads;
+    f.total_tokens = total_tokens;
+    f.sign = -1.f;
+    f.status = status;
+    return launch_norm_rope(f, head_dim, interleaved != 0, dev.num_sms, s) == cudaSuccess
+               ? CPATTN_OK
+               : CPATTN_ERR_CUDA;
+  }
   NormRopeBwdParams p{};
   p.dq_out = static_cast<const __nv_bfloat16*>(dq_out);
   p.dk_out = static_cast<const __nv_bfloat16*>(dk_out);
@@ -273,7 +299,7 @@ extern "C" int cpattn_qk_norm_rope_bwd(
   p.status = status;
   p.partial = static_cast<float*>(workspace);
   return launch_norm_rope_bwd(p, head_dim, interleaved != 0, dq_weight, dk_weight, dev.num_sms,
-                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+                              s) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
 }
@@ -338,6 +364,7 @@ extern "C" int cpattn_paged_append(
   p.kv_heads = num_kv_heads;
   p.total_tokens = total_tokens;
   p.eps = eps;
+  p.sign = 1.f;
   p.status = status;
   p.cu_seqlens = cu_seqlens;
   p.kv_lens = kv_lens;
