@@ -470,14 +470,19 @@ static cudaError_t launch_norm_rope_d(const NormRopeParams& p, bool interleaved,
   };
   // Eight heads a lane group share a position's angles and have four times the
   // loads in flight of two (16,384 tokens of 64 heads: 87 us, four heads 103 us,
-  // sixteen 92 us), as long as they leave every SM several rounds of CTAs; a
-  // decoding step wants its few rows spread out (32 tokens of 40 heads: two heads
-  // 4.8 us, four 6.1 us).
+  // sixteen 92 us), as long as they leave every SM several rounds of CTAs (a
+  // decoding step wants its few rows spread out, 32 tokens of 40 heads: two heads
+  // 4.8 us, four 6.1 us) and at most half of their places go unused (32,768
+  // tokens of 3 + 1 heads, three quarters: 24.7 us, in runs of four 18.5 us; of
+  // 5 + 5 heads, three eighths: 18.6 us, in runs of two 24.7 us).
   const long long many = 12LL * num_sms * (kNrThreads / (D / 8));
   if (units_at(1) == 0) return cudaSuccess;
-  if (units_at(4 * kUnit) >= many)
+  auto fits = [&](int run) {
+    return units_at(run) >= many && units_at(run) * run <= 2 * units_at(1);
+  };
+  if (fits(4 * kUnit))
     return launch_norm_rope_t<D, 4>(p, interleaved, units_at(4 * kUnit), stream);
-  if (units_at(2 * kUnit) >= many)
+  if (fits(2 * kUnit))
     return launch_norm_rope_t<D, 2>(p, interleaved, units_at(2 * kUnit), stream);
   return launch_norm_rope_t<D, 1>(p, interleaved, units_at(kUnit), stream);
 }
