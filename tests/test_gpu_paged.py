@@ -428,3 +428,71 @@ def test_a_cache_past_32_bit_offsets(cp):
     cp.paged_append(k, v, kc, vc, t, cu, kv)
     for (i, _, _, page, row) in op.places(x.cu, x.kv, table_, size)[::37]:
         assert torch.equal(kc[page, row], k[i]) and torch.equal(vc[page, row], v[i])
+
+
+def test_refused_tensors(cp):
+    """Types, shapes and layouts are refused before anything is enqueued."""
+    x = Batch([2, 1], [40, 20], 4, 2, 64, 16, seed=19)
+    q, kc, vc, t, cu, kv = x.on_gpu()
+    k = normal(3, 2, 64, seed=1).cuda()
+    pos, tab = torch.zeros(3, dtype=torch.int32, device="cuda"), table(8, 64).cuda()
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    good = dict(q=q, k_cache=kc, v_cache=vc, page_table=t, cu_seqlens=cu, kv_lens=kv)
+    bounds = dict(max_seqlen=2, max_kv_len=40)
+    stacked = torch.stack([kc, vc], 1)
+    for change, error in (
+            (dict(q=q.float()), TypeError), (dict(q=q.cpu()), ValueError),
+            (dict(q=q.transpose(0, 1)), ValueError), (dict(q=q[:, ::2]), ValueError),
+            (dict(q=q[..., :32]), ValueError), (dict(q=q[0]), ValueError),
+            (dict(k_cache=kc.half()), TypeError), (dict(k_cache=kc[:-1]), ValueError),
+            (dict(v_cache=vc.transpose(1, 2)), ValueError), (dict(k_cache=kc[..., 0]), ValueError),
+            (dict(k_cache=stacked[:, 0]), ValueError),           # another page stride than v's
+            (dict(page_table=t.long()), TypeError), (dict(page_table=t[:1]), ValueError),
+            (dict(page_table=t[:, ::2]), ValueError), (dict(page_table=t[0]), ValueError),
+            (dict(cu_seqlens=cu[:-1]), ValueError), (dict(kv_lens=kv.long()), TypeError),
+            (dict(kv_lens=kv[None]), ValueError), (dict(q=None), TypeError)):
+        with pytest.raises(error):
+            cp.paged_attn(**{**good, **change}, **bounds)
+    for change, error in ((dict(out=q[:2]), ValueError), (dict(out=q.float()), TypeError),
+                          (dict(lse=torch.zeros(3, 4, device="cuda").double()), TypeError),
+                          (dict(workspace=torch.zeros(64, device="cuda")), TypeError),
+                          (dict(max_seqlen=1 << 40), ValueError), (dict(max_kv_len="x"), TypeError),
+                          (dict(softmax_scale="x"), TypeError), (dict(stream=3), AttributeError)):
+        with pytest.raises(error):
+            cp.paged_attn(**good, **{**bounds, **change})
+    for change, status in ((dict(out=q), cp.ERR_INVALID_ARG),
+                           (dict(softmax_scale=-1.0), cp.ERR_INVALID_ARG),
+                           (dict(workspace=torch.zeros(512, dtype=torch.uint8, device="cuda")),
+                            cp.ERR_WORKSPACE_TOO_SMALL)):
+        with pytest.raises(cp.CpattnError) as e:
+            cp.paged_attn(**good, **{**bounds, **change})
+        assert e.value.status == status
+    for args, kw, error in (
+            ((k, k[:2], kc, vc, t, cu, kv), {}, ValueError),
+            ((k, k, kc, vc, t, cu, kv), dict(q_weight=w), ValueError),
+            ((k, k, kc, vc, t, cu, kv), dict(rope_table=tab[0]), ValueError),
+            ((k, k, kc, vc, t, cu, kv), dict(rope_table=tab.double()), TypeError),
+            ((k, k, kc, vc, t, cu, kv), dict(k_weight=w[:32]), ValueError),
+            ((k, k, kc[:, :, :1], vc[:, :, :1], t, cu, kv), {}, ValueError),
+            ((k, k, kc, kc, t, cu, kv), {}, cp.CpattnError),     # one cache for both
+            ((k[:, :, :32].contiguous(),) * 2 + (kc, vc, t, cu, kv), {}, ValueError),
+            ((k.transpose(0, 1).contiguous().transpose(0, 1), k, kc, vc, t, cu, kv), {}, ValueError)):
+        with pytest.raises(error):
+            cp.paged_append(*args, **kw)
+    for args, kw, error in (
+            ((q, k, pos.long(), tab), {}, TypeError), ((q, k, pos[:2], tab), {}, ValueError),
+            ((q, k[:2], pos, tab), {}, ValueError), ((q, k, None, tab), {}, TypeError),
+            ((q, k, pos, tab), dict(q_weight=w), cp.CpattnError),  # one weight of two
+            ((q, k, None, None), {}, cp.CpattnError),              # nothing to do
+            ((q[:1].expand(3, 4, 64), k, pos, tab), {}, cp.CpattnError),
+            ((q, k, pos, tab), dict(q_out=q[:2]), ValueError),
+            ((q, k, pos, tab), dict(status=pos), ValueError),
+            ((q, k, pos, table(8, 40).cuda()), {}, cp.CpattnError)):
+        with pytest.raises(error):
+            cp.qk_norm_rope(*args, **kw)
+    with pytest.raises(ValueError):
+        cp.qk_norm_rope_bwd(q, k, q, k, pos, tab, dq_weight=torch.zeros(64, device="cuda"))
+    with pytest.raises(TypeError):
+        cp.qk_norm_rope_bwd(q, k, None, None, pos, tab, q_weight=w, k_weight=w)
+    out, lse = cp.paged_attn(**good, **bounds)
+    x.check(out, lse)
