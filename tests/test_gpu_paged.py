@@ -118,6 +118,7 @@ def test_attention(cp, new, kv, H, Hk, D, size, causal):
     ([4], [5000], 16, 2, 128, 16, 1.0),
     ([5], [20000], 5, 1, 64, 64, 1.0),                   # more splits than a round of the merge
     ([100, 60], [2600, 2000], 4, 4, 64, 16, 2.0),        # tiles cut at several places
+    ([300, 10, 0, 700], [2300, 1800, 5, 2000], 16, 16, 64, 16, 1.0),  # more pieces than SMs
 ])
 def test_long_caches(cp, new, kv, H, Hk, D, size, std):
     x = Batch(new, kv, H, Hk, D, size, seed=3, std=std)
