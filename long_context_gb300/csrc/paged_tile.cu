@@ -19,13 +19,16 @@
 //                   until its queued MMAs drain, and releases it through a named
 //                   barrier; it also clears what the last V tile holds behind
 //                   the cache's end (weight 0 times a NaN there would be NaN)
-// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 and O1 at 256 + t*D.  P_t
-// (bf16, two per column) overwrites the first 64 columns of S_t at head size
-// 128, so S of the next key tile follows PV of this one and a Q tile's chain is
+// TMEM (512 columns) at head size 128: S0 [0,128), S1 [128,256), O0 and O1 at
+// 256 + t*D.  P_t (bf16, two per column) overwrites the first 64 columns of S_t,
+// so S of the next key tile follows PV of this one and a Q tile's chain is
 // softmax, hand-over, PV and S (about 2,900 cycles a key tile, of which the
-// tensor pipe works 2,048 for two Q tiles).  At head size 64 the columns suffice
-// for a P of its own (384 + t*64): the softmax hands S back once it is in
-// registers and the next S is computed during the exponentials.
+// tensor pipe works 2,048 for two Q tiles).  Head size 64 has columns for three
+// S: the products of both Q tiles take the buffers in turn, P again inside its S,
+// and S of a Q tile's next key tile is there before its softmax needs it (4,864
+// tokens over 32,768, 16 heads of 64: 724 us; with two S and a P of its own, S
+// given back after the exponentials, 741 us, before them and so with a maximum of
+// every tile, 783 us).
 //
 // Softmax: p = 2^(s scale log2 e - m) with a running reference m per row that
 // only has to keep p below 2^16 (O and l share it, so O / l and m + ln l do not
@@ -54,22 +57,22 @@ struct TileCfg {
   static constexpr int kHalves = D / 64;          // 128-byte swizzle atoms
   static constexpr int kTileBytes = 128 * D * 2;  // one 128-row bf16 tile
   static constexpr int kStages = (D == 64) ? 4 : 2;
+  // Head size 64 leaves TMEM columns for a third S: product s (of tile s / nq and
+  // Q tile s % nq) goes to buffer s % 3.
+  static constexpr bool kRing = D == 64;
+  static constexpr int kBufs = kRing ? 3 : kNQ;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kNQ * kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kBarOff = kVOff + kStages * kTileBytes;
   // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[NQ],
-  // p_full[NQ], o_done[NQ], drain, staged[NQ], s_read[NQ]
-  static constexpr int kNumBars = 1 + 4 * kStages + 3 * kNQ + 1 + 2 * kNQ;
+  // p_full[NQ], o_done[NQ], drain, staged[NQ]; s_full[kBufs] instead with a ring
+  static constexpr int kNumBars = 1 + 4 * kStages + kBufs + 2 * kNQ + 1 + kNQ;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;  // + align slack
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kOCol = 2 * kBN;
-  // Head size 64 leaves TMEM columns for a P of its own, so that S is free as
-  // soon as the softmax has read it.
-  static constexpr bool kOwnP = D == 64;
-  static constexpr uint32_t kPCol = kOwnP ? kOCol + kNQ * D : 0;
-  static constexpr uint32_t kPStep = kOwnP ? kBN / 2 : kBN;
+  static constexpr uint32_t kOCol = kBufs * kBN;
+  static_assert(kOCol + kNQ * D <= kTmemCols);
 };
 
 // Byte offset of 16-byte chunk c of row r in a tile stored as 64-column
@@ -134,11 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + C::kStages;
   uint64_t* v_empty = v_full + C::kStages;
   uint64_t* s_full = v_empty + C::kStages;
-  uint64_t* p_full = s_full + kNQ;
+  uint64_t* p_full = s_full + C::kBufs;
   uint64_t* o_done = p_full + kNQ;
   uint64_t* drain = o_done + kNQ;
   uint64_t* staged = drain + 1;  // O tile t staged in shared memory (128 arrivals)
-  uint64_t* s_read = staged + kNQ;  // kOwnP: S_t is in registers (128 arrivals)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
 
@@ -187,10 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&o_done[t], 1);
       }
       mbar_init(drain, 1);
-      for (int t = 0; t < kNQ; ++t) {
-        mbar_init(&staged[t], kBM);
-        mbar_init(&s_read[t], kBM);
-      }
+      for (int t = 0; t < kNQ; ++t) mbar_init(&staged[t], kBM);
+      for (int b = kNQ; b < C::kBufs; ++b) mbar_init(&s_full[b], 1);
       *abort_flag = 0;
       fence_mbarrier_init();
       tma_prefetch_desc(&tm_q);
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024));
       const uint32_t lo_v =
           static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kVOff), 16384, 1024));
-      auto issue_s = [&](int t, int st) {
-        const uint32_t d = tmem + t * kBN;
+      auto issue_s = [&](int t, int st, int buf) {
+        const uint32_t d = tmem + buf * kBN;
         const uint32_t a0 = lo_q + t * (C::kTileBytes >> 4);
         const uint32_t b0 = lo_k + st * (C::kTileBytes >> 4);
 #pragma unroll
@@ -283,60 +283,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(d, pack_u64(a0 + off, hi_kq), pack_u64(b0 + off, hi_kq), idesc_s,
                  kk > 0 ? 1u : 0u);
         }
-        mma_commit(&s_full[t]);
+        mma_commit(&s_full[buf]);
       };
-      auto issue_pv = [&](int t, int st, bool acc) {
+      auto issue_pv = [&](int t, int st, int buf, bool acc) {
         const uint32_t d = tmem + C::kOCol + t * D;
-        const uint32_t a = tmem + C::kPCol + t * C::kPStep;
+        const uint32_t a = tmem + buf * kBN;
         const uint32_t b0 = lo_v + st * (C::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           mma_ts(d, a + kk * 8, pack_u64(b0 + ((kk * 2048) >> 4), hi_v), idesc_o,
                  (acc || kk > 0) ? 1u : 0u);
       };
-      named_bar_sync(1, 64);  // Q and K(0) landed
-      if (lane == 0 && n > 0) {
-        tc_fence_after();
-        for (int t = 0; t < nq; ++t) issue_s(t, 0);
-        mma_commit(&k_empty[0]);
-      }
-      __syncwarp();
-      for (int x = 0; x < n; ++x) {
-        const int st = x % C::kStages;
-        const bool has_next = x + 1 < n;
-        const int st1 = (x + 1) % C::kStages;
-        if constexpr (C::kOwnP) {
-          if (has_next) {
-            for (int t = 0; t < nq; ++t) {
-              named_bar_sync(1, 64);  // S_t(x) was read and K(x+1) is ready
-              if (lane == 0) {
-                tc_fence_after();
-                issue_s(t, st1);
-                if (t == nq - 1) mma_commit(&k_empty[st1]);
-              }
-              __syncwarp();
-            }
+      if constexpr (C::kRing) {
+        // The first three products of Q and K, then after P_s's product with V the
+        // product s + 3 into the buffer that P_s leaves (in issue order).
+        const int total = n * nq;
+        auto next_s = [&](int s) {
+          const int x = s / nq, t = s - x * nq, st = x % C::kStages;
+          issue_s(t, st, s % C::kBufs);
+          if (t == nq - 1) mma_commit(&k_empty[st]);
+        };
+        for (int s = 0; s < min(total, C::kBufs); ++s) {
+          named_bar_sync(1, 64);  // Q and its K landed
+          if (lane == 0) {
+            tc_fence_after();
+            next_s(s);
           }
-          for (int t = 0; t < nq; ++t) {
-            named_bar_sync(1, 64);  // P_t(x) and V(x) are ready
-            if (lane == 0) {
-              tc_fence_after();
-              issue_pv(t, st, x > 0);
-              mma_commit(&o_done[t]);  // every tile: P_t may be overwritten
-              if (t == nq - 1) mma_commit(&v_empty[st]);
-            }
-            __syncwarp();
+          __syncwarp();
+        }
+        for (int s = 0; s < total; ++s) {
+          named_bar_sync(1, 64);  // P_s, its V and the K of product s + 3 are ready
+          if (lane == 0) {
+            tc_fence_after();
+            const int x = s / nq, t = s - x * nq, st = x % C::kStages;
+            issue_pv(t, st, s % C::kBufs, x > 0);
+            mma_commit(&o_done[t]);
+            if (t == nq - 1) mma_commit(&v_empty[st]);
+            if (s + C::kBufs < total) next_s(s + C::kBufs);
           }
-        } else {
+          __syncwarp();
+        }
+      } else {
+        named_bar_sync(1, 64);  // Q and K(0) landed
+        if (lane == 0 && n > 0) {
+          tc_fence_after();
+          for (int t = 0; t < nq; ++t) issue_s(t, 0, t);
+          mma_commit(&k_empty[0]);
+        }
+        __syncwarp();
+        for (int x = 0; x < n; ++x) {
+          const int st = x % C::kStages;
+          const bool has_next = x + 1 < n;
+          const int st1 = (x + 1) % C::kStages;
           for (int t = 0; t < nq; ++t) {
             named_bar_sync(1, 64);  // P_t(x), V(x) and K(x+1) are ready
             if (lane == 0) {
               tc_fence_after();
-              issue_pv(t, st, x > 0);
+              issue_pv(t, st, t, x > 0);
               if (!has_next) mma_commit(&o_done[t]);
               if (t == nq - 1) mma_commit(&v_empty[st]);
               if (has_next) {
-                issue_s(t, st1);
+                issue_s(t, st1, t);
                 if (t == nq - 1) mma_commit(&k_empty[st1]);
               }
             }
@@ -354,47 +361,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       // After a failed (bounded) wait the remaining rendezvous still happen,
       // without waiting, so the MMA warp always runs to its end.
       bool ok = true;
-      if (lane == 0) {
-        ok = wait_bounded(q_full, 0, abort_flag);
-        if (ok && n > 0) ok = wait_bounded(&k_full[0], 0, abort_flag);
-      }
-      __syncwarp();
-      named_bar_sync(1, 64);
-      for (int x = 0; x < n; ++x) {
-        const int st = x % C::kStages;
-        const uint32_t ph = (x / C::kStages) & 1;
-        const int st1 = (x + 1) % C::kStages;
-        const uint32_t ph1 = ((x + 1) / C::kStages) & 1;
-        if (C::kOwnP && x + 1 < n) {
-          if (lane == 0 && ok) ok = wait_bounded(&k_full[st1], ph1, abort_flag);
+      auto clear_v = [&](int x) {
+        const int used = kv_len - (kv_lo + x * kBN);
+        if (used < kBN) {
+          // The cache ends in this tile: clear V behind it (and tell the
+          // tensor core's proxy).
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          uint8_t* v = smem + C::kVOff + (x % C::kStages) * C::kTileBytes;
+          for (int i = used * 8 + lane; i < kBN * 8; i += 32)
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              *reinterpret_cast<uint4*>(v + hf * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      };
+      if constexpr (C::kRing) {
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (lane == 0 && ok) ok = wait_bounded(bar, parity, abort_flag);
+        };
+        auto wait_k = [&](int x) { wait(&k_full[x % C::kStages], (x / C::kStages) & 1); };
+        wait(q_full, 0);
+        const int total = n * nq;
+        for (int s = 0; s < min(total, C::kBufs); ++s) {
+          wait_k(s / nq);
+          __syncwarp();
+          named_bar_sync(1, 64);
+        }
+        for (int s = 0; s < total; ++s) {
+          const int x = s / nq, t = s - x * nq;
+          if (t == 0) {
+            wait(&v_full[x % C::kStages], (x / C::kStages) & 1);
+            clear_v(x);
+          }
+          if (s + C::kBufs < total) wait_k((s + C::kBufs) / nq);
+          wait(&p_full[t], x & 1);
+          __syncwarp();
+          named_bar_sync(1, 64);
+        }
+      } else {
+        if (lane == 0) {
+          ok = wait_bounded(q_full, 0, abort_flag);
+          if (ok && n > 0) ok = wait_bounded(&k_full[0], 0, abort_flag);
+        }
+        __syncwarp();
+        named_bar_sync(1, 64);
+        for (int x = 0; x < n; ++x) {
+          const int st = x % C::kStages;
+          const uint32_t ph = (x / C::kStages) & 1;
+          const int st1 = (x + 1) % C::kStages;
+          const uint32_t ph1 = ((x + 1) / C::kStages) & 1;
           for (int t = 0; t < nq; ++t) {
-            if (lane == 0 && ok) ok = wait_bounded(&s_read[t], x & 1, abort_flag);
+            if (t == 0) {
+              if (lane == 0 && ok) ok = wait_bounded(&v_full[st], ph, abort_flag);
+              clear_v(x);
+              if (lane == 0 && ok && x + 1 < n)
+                ok = wait_bounded(&k_full[st1], ph1, abort_flag);
+            }
+            if (lane == 0 && ok) ok = wait_bounded(&p_full[t], x & 1, abort_flag);
             __syncwarp();
             named_bar_sync(1, 64);
           }
-        }
-        for (int t = 0; t < nq; ++t) {
-          if (t == 0) {
-            if (lane == 0 && ok) ok = wait_bounded(&v_full[st], ph, abort_flag);
-            const int used = kv_len - (kv_lo + x * kBN);
-            if (used < kBN) {
-              // The cache ends in this tile: clear V behind it (and tell the
-              // tensor core's proxy).
-              ok = __shfl_sync(0xffffffffu, ok, 0);
-              uint8_t* v = smem + C::kVOff + st * C::kTileBytes;
-              for (int i = used * 8 + lane; i < kBN * 8; i += 32)
-#pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
-                  *reinterpret_cast<uint4*>(v + hf * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            if (!C::kOwnP && lane == 0 && ok && x + 1 < n)
-              ok = wait_bounded(&k_full[st1], ph1, abort_flag);
-          }
-          if (lane == 0 && ok) ok = wait_bounded(&p_full[t], x & 1, abort_flag);
-          __syncwarp();
-          named_bar_sync(1, 64);
         }
       }
       if (lane == 0 && !ok) {
@@ -410,9 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = warp >> 2;
       const int r = threadIdx.x & 127;
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t s_addr = tmem + lane_base + t * kBN;
       const uint32_t o_addr = tmem + lane_base + C::kOCol + t * D;
-      const uint32_t p_addr = tmem + lane_base + C::kPCol + t * C::kPStep;
       const int my_tok = tok_lo + t * tile_toks + r / G;
       const bool row_valid = r < tile_rows && my_tok >= 0;
       // Keys below lim are visible; a row that is not there sees none, and
@@ -424,13 +449,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
 
       for (int x = 0; x < n; ++x) {
-        ok = __all_sync(0xffffffffu, wait_bounded(&s_full[t], x & 1, abort_flag));
+        // P goes where S was.
+        const int s = x * nq + t;
+        const int buf = C::kRing ? s % C::kBufs : t;
+        const uint32_t s_addr = tmem + lane_base + buf * kBN;
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded(&s_full[buf], (C::kRing ? s / C::kBufs : x) & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        // S is still in TMEM for a second pass: P is written after it.  With a P
-        // of its own S is given back before the exponentials, so there the
-        // maximum is always taken.
-        bool with_max = C::kOwnP || __any_sync(0xffffffffu, m_run == kNegInfT);
+        // S is still in TMEM for a second pass: P is written after it.
+        bool with_max = __any_sync(0xffffffffu, m_run == kNegInfT);
         float2 acc0, acc1;
         uint32_t pk[kBN / 2];
 #pragma unroll 1
@@ -441,10 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < kBN / 32; ++q) reg_fence32(sr + q * 32);
-          if (C::kOwnP) {
-            tc_fence_before();
-            mbar_arrive(&s_read[t]);
-          }
 
           // Visible keys of this row form a prefix of the tile.
           const int nvis = lim - (kv_lo + x * kBN);
@@ -469,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m_new = fmaxf(m_run, m_tile);
             if (__any_sync(0xffffffffu, m_new > m_run + kMoveByT)) {
               const float alpha = (m_run == kNegInfT) ? 0.f : ex2_approx(m_run - m_new);
-              if (C::kOwnP && x > 0) {
+              if (C::kRing && x > 0) {
                 ok = __all_sync(0xffffffffu, wait_bounded(&o_done[t], (x - 1) & 1, abort_flag));
                 tc_fence_after();
               }
@@ -512,21 +536,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           with_max = true;
         }
         l_run += (acc0.x + acc1.x) + (acc0.y + acc1.y);
-        if (C::kOwnP && x > 0) {  // PV of the previous tile has read P
+        if (C::kRing && x > 0) {  // one phase of o_done[t] at a time: its parity tells only two
           ok = __all_sync(0xffffffffu,
                           ok && wait_bounded(&o_done[t], (x - 1) & 1, abort_flag));
           if (!ok) break;
           tc_fence_after();
         }
-        tmem_st32(p_addr, pk);
-        tmem_st32(p_addr + 32, pk + 32);
+        tmem_st32(s_addr, pk);
+        tmem_st32(s_addr + 32, pk + 32);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[t]);
       }
       if (ok && n > 0) {
         ok = __all_sync(0xffffffffu,
-                        wait_bounded(&o_done[t], C::kOwnP ? (n - 1) & 1 : 0, abort_flag));
+                        wait_bounded(&o_done[t], C::kRing ? (n - 1) & 1 : 0, abort_flag));
         tc_fence_after();
       }
       if (ok) {
