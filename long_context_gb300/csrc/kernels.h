@@ -286,6 +286,7 @@ struct PagedShape {
   int unit;        // keys of a unit
   int min_units;   // tiles, and few rows of many items: a split has at least so many units
   int whole;       // items of up to so many units stay whole
+  int keep;        // and lists that have no larger items than this
   int ctas;        // a split does at least 1 / ctas of the whole work
   int round;       // CTAs resident at once (at most ctas)
   bool join;       // the last CTA of a split item joins it (else a merge kernel)

@@ -7,17 +7,19 @@
 // Few rows (HBM bound; two CTAs a SM): an item of u units becomes
 // ceil(u / target) equal splits (see paged_rows_target).
 //
-// Tiles (one CTA a SM, an item is up to hundreds of units): the items' units are
-// laid end to end and cut at every multiple of one SM's share
-// C = max(min_units, ceil(W heads / SMs)), unless the cut would fall within C / 16
-// of an item's end or the item has at most eight units (or, when an eighth of the
-// work is in items of less than C / 4, at most C).  So items that divide badly among the SMs are evened out by
-// at most one cut a SM, and the splits are listed by decreasing size, which the
-// hardware then starts in that order as SMs become free.  (Measured on 152 SMs:
-// 2,048 tokens over 32,768, 256 items of 272 units, 740 us, uncut 826 us; a whole
-// prompt of 8,192 tokens, 512 items of 2 to 64 units, 206 us uncut and 221 us cut,
-// hence the rule for small items; ragged chunks, 292 items of 1 to 44 units, 79 us,
-// uncut 87 us.)
+// Tiles (one CTA a SM, an item is up to hundreds of units): left whole, the items
+// go to the SMs by decreasing size, and the last SM is done after about
+//   E = max over k of (k + 1) p[k SMs],  p the sizes in decreasing order from p[0]
+// (k + 1 items as large as p[k SMs] meet on some SM).  Cut, every SM has
+// C = W heads / SMs units and the merge and the pieces' starts to pay, about
+// `keep` = 14 units; so the items are cut when 65 / 64 E > C + 14.  (D = 128, us
+// uncut and cut: C 458, E 544: 829 and 745; C 188, E 200: 359 and 341; C 1.5, E 16:
+// 40 and 31; C 54, E 67: 120 and 130; C 10, E 22: 47 and 52; C 318, E 321: 545 and
+// 564.  D = 64: C 31, E 50: 77 and 65; C 22, E 26: 48 and 60.)
+// Then the items' units are laid end to end and cut at every multiple of
+// max(min_units, C), unless the cut would fall within C / 16 of an item's end or
+// the item has no more than `whole` units, and the splits are listed by decreasing
+// size.
 //
 // Either way the split items have at most 2 ctas / heads splits in all (an item
 // of n > 1 splits has more than (n - 1) target units, or n - 1 cuts), which
@@ -37,6 +39,7 @@ namespace {
 
 constexpr int kPmThreads = 256;
 constexpr int kBuckets = 128;  // sizes told apart in the list's order (at most NT)
+constexpr int kMeet = 3;       // k up to which E is taken (beyond it is close to C)
 constexpr float kNegInfP = -__builtin_huge_valf();
 
 // Inclusive scan over the block; warp_sums[NT / 32 - 1] holds the total after it.
@@ -86,8 +89,8 @@ __device__ __forceinline__ PagedItem paged_item(const PagedParams& p, const int*
   t.kv_len = p.kv_lens[t.seq];
   const int n_blk = first[t.seq + 1] - first[t.seq];
   t.blk = n_blk - 1 - (i - first[t.seq]);  // costly blocks first
-  const long long row_hi =
-      static_cast<long long>(t.q_len) * p.group - (n_blk - 1 - t.blk) * static_cast<long long>(p.shape.rows);
+  const long long row_hi = static_cast<long long>(t.q_len) * p.group -
+                           (n_blk - 1 - t.blk) * static_cast<long long>(p.shape.rows);
   const int last_tok = static_cast<int>((row_hi - 1) / p.group);
   t.hi = p.causal ? max(t.kv_len - t.q_len + last_tok + 1, 0) : t.kv_len;
   return t;
@@ -99,13 +102,17 @@ __device__ __forceinline__ int paged_tiles_target(const PagedShape& s, long long
   return static_cast<int>(min(max(share, static_cast<long long>(s.min_units)), 1ll << 30));
 }
 
-// Cuts of the item that is units [at, at + units) of all laid end to end.  When
-// small items hold an eighth of the work (`even`), they even out the SMs by
-// themselves, and only items above a share are cut.
-__device__ __forceinline__ int paged_cuts(const PagedShape& s, long long at, int units, int target,
-                                          bool even) {
+// Whether tiles are cut: the estimate of the uncut time against the share.
+__device__ __forceinline__ bool paged_cut(const PagedShape& s, long long all, int heads,
+                                          long long uncut) {
+  return uncut * 65 * s.ctas > (all * heads + static_cast<long long>(s.keep) * s.ctas) * 64;
+}
+
+// Cuts of the item that is units [at, at + units) of all laid end to end.
+__device__ __forceinline__ int paged_cuts(const PagedShape& s, long long at, int units,
+                                          int target) {
   const int snap = target / 16 + 1;
-  if (units <= (even ? max(target, s.whole) : s.whole)) return 0;
+  if (units <= s.whole) return 0;
   const long long m0 = (at + snap) / target + 1;
   const long long m1 = (at + units - snap - 1) / target;
   return m1 >= m0 ? static_cast<int>(m1 - m0) + 1 : 0;
@@ -113,6 +120,13 @@ __device__ __forceinline__ int paged_cuts(const PagedShape& s, long long at, int
 
 __device__ __forceinline__ int item_units(const PagedParams& p, const PagedItem& t) {
   return (t.hi + p.shape.unit - 1) / p.shape.unit;
+}
+
+// Which of kBuckets equal ranges of [0, largest] holds `units` (below 2^24, as
+// units of 128 keys are).
+__device__ __forceinline__ int size_bucket(int units, int largest) {
+  return min(kBuckets - 1, static_cast<int>(static_cast<unsigned>(units) * kBuckets /
+                                            (static_cast<unsigned>(largest) + 1)));
 }
 
 }  // namespace
@@ -185,10 +199,24 @@ __global__ void __launch_bounds__(128) paged_schedule_few_kernel(const PagedPara
   const long long at = upto - units, all = __shfl_sync(0xffffffffu, upto, 31);
   const int target = paged_tiles_target(p.shape, all, p.num_kv_heads);
   const int snap = target / 16 + 1;
-  long long small_sum = units <= target / 4 ? units : 0;
+  const int top = __reduce_max_sync(0xffffffffu, units);
+  bool cutting = false;
+  if (top > p.shape.keep) {
+    int rank = 0;  // by decreasing size
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) small_sum += __shfl_xor_sync(0xffffffffu, small_sum, o);
-  const int n = have ? paged_cuts(p.shape, at, units, target, small_sum * 8 >= all) + 1 : 0;
+    for (int o = 0; o < 32; ++o) {
+      const int u = __shfl_sync(0xffffffffu, units, o);
+      rank += u > units || (u == units && o < lane);
+    }
+    // This item's bound of the uncut time, if its rank gives one.
+    int uncut = 0;
+#pragma unroll
+    for (int k = 0; k <= kMeet; ++k)
+      if (have && rank == k * p.shape.ctas / p.num_kv_heads) uncut = (k + 1) * units;
+    uncut = __reduce_max_sync(0xffffffffu, uncut);
+    cutting = paged_cut(p.shape, all, p.num_kv_heads, uncut);
+  }
+  const int n = have ? (cutting ? paged_cuts(p.shape, at, units, target) : 0) + 1 : 0;
   const int cut = n > 1 ? static_cast<int>(((at + snap) / target + 1) * target - at) : units;
   const long long v = n + (n > 1 ? (static_cast<long long>(n) << 32) + (1ll << 48) : 0);
   const long long after = scan(v), before = after - v;
@@ -265,13 +293,15 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   __shared__ int s_base[kPsThreads + 1];   // first split of each item of a round
   __shared__ int s_bucket[kBuckets];       // splits by size
   __shared__ long long s_round;
+  __shared__ int s_top;
   __shared__ PagedItem s_item[kPsThreads];
   __shared__ int2 s_split[kPsThreads];     // units of the first split, first slot (-1: whole)
   __shared__ int s_number[kPsThreads];     // number among the split items
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const int B = p.num_seqs;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_top = 0;
+  for (int i = tid; i < kBuckets; i += kPsThreads) s_bucket[i] = 0;
   __syncthreads();
 
   // Items of each sequence, and the checks that need device memory.
@@ -309,28 +339,44 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   // All units, and the largest split that shares them out.
   const bool tiles = p.shape.tiles;
   long long sum = 0;
+  int most = 0;
   PagedItem it = {};
   for (int i = tid; i < items; i += kPsThreads) {
     it = paged_item(p, first, i);
-    sum += item_units(p, it);
+    const int units = item_units(p, it);
+    sum += units;
+    most = max(most, units);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMax(&s_top, most);
   ps_scan<NT>(sum, warp_sums);
   const long long all = warp_sums[NT / 32 - 1];
   const int target = tiles ? paged_tiles_target(p.shape, all, p.num_kv_heads)
                            : paged_rows_target(p.shape, all, items, p.num_kv_heads);
   const int snap = target / 16 + 1;
-  bool even = false;
-  if (tiles) {
-    long long small_sum = 0;
-    __syncthreads();
+  const int top = s_top;
+  bool cutting = false;
+  if (tiles && top > p.shape.keep) {
+    // The items by size, and from that the estimate of the uncut time.
     for (int i = tid; i < items; i += kPsThreads) {
       if (items > kPsThreads) it = paged_item(p, first, i);
-      const int units = item_units(p, it);
-      if (units <= target / 4) small_sum += units;
+      atomicAdd(&s_bucket[kBuckets - 1 - size_bucket(item_units(p, it), top)], 1);
     }
-    ps_scan<NT>(small_sum, warp_sums);
-    even = warp_sums[NT / 32 - 1] * 8 >= all;
+    __syncthreads();
+    // Thread b: items in the buckets up to its own, the larger sizes first.
+    const int mine = tid < kBuckets ? s_bucket[tid] : 0;
+    const int upto = static_cast<int>(ps_scan<NT>(mine, warp_sums));
+    for (int k = 1; k <= kMeet; ++k) {
+      const int rank = k * p.shape.ctas / p.num_kv_heads;
+      const unsigned size = (kBuckets - 1u - tid) * (top + 1u) / kBuckets;
+      if (upto - mine <= rank && rank < upto)
+        atomicMax(&s_top, (k + 1) * static_cast<int>(size));
+    }
+    __syncthreads();
+    cutting = paged_cut(p.shape, all, p.num_kv_heads, s_top);
   }
+  // No split has more units.
+  const int largest = cutting ? max(target + 2 * snap, p.shape.whole) : top;
   for (int i = tid; i < kBuckets; i += kPsThreads) s_bucket[i] = 0;
   __syncthreads();
 
@@ -356,7 +402,7 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
           unit0 += warp_sums[NT / 32 - 1];
           __syncthreads();
           if (i < items) {
-            n = paged_cuts(p.shape, at, units, target, even) + 1;
+            n = (cutting ? paged_cuts(p.shape, at, units, target) : 0) + 1;
             cut = n > 1 ? static_cast<int>(((at + snap) / target + 1) * target - at) : units;
           }
         } else if (i < items) {
@@ -411,9 +457,7 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
         const int units = item_units(p, t);
         const int u0 = s == 0 ? 0 : sp.x + (s - 1) * step;
         const int u1 = s == n - 1 ? units : sp.x + s * step;
-        const int bucket =
-            min(kBuckets - 1, static_cast<int>((u1 - u0) * static_cast<long long>(kBuckets) /
-                                               (target + 2 * snap)));
+        const int bucket = size_bucket(u1 - u0, largest);
         if (pass == 0) {
           atomicAdd(&s_bucket[kBuckets - 1 - bucket], 1);
           continue;

@@ -66,17 +66,19 @@ PagedShape paged_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   if (s.tiles) {
     s.rows = kNQ * static_cast<int>(kBM / group * group);
     s.unit = kBN;
-    // A key tile takes 1.5 us and a cut costs about 6 us (the merge): pieces of
-    // four tiles pay for items above eight.
+    // A key tile takes 1.4-1.5 us and cutting a list about as long as 14 of them
+    // (the schedule has the figures).  In a list that is cut, pieces of four tiles
+    // pay for items above eight (an item of 19 among 28: 30 us, cut above 14: 40 us).
     s.min_units = 4;
     s.whole = 8;
+    s.keep = 14;
     s.ctas = 152;
     s.round = 152;
   } else {
     s.rows = rows <= 16 ? 16 : 32;
     s.unit = 64;
     s.min_units = 24;
-    s.whole = 1;
+    s.whole = s.keep = 1;
     s.ctas = 608;
     s.round = 304;
   }
@@ -496,8 +498,8 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   } else if (launch_paged_rows(p, head_dim, s) != cudaSuccess) {
     return CPATTN_ERR_CUDA;
   }
-  // Short items are never split; after a plan the merge also writes the error word.
-  if (!p.shape.join && (p.shape.plan || max_kv_len > p.shape.whole * p.shape.unit) &&
+  // Lists of short items are never cut; after a plan the merge also writes the error word.
+  if (!p.shape.join && (p.shape.plan || max_kv_len > p.shape.keep * p.shape.unit) &&
       launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   return CPATTN_OK;

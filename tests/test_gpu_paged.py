@@ -119,6 +119,10 @@ def test_attention(cp, new, kv, H, Hk, D, size, causal):
     ([5], [20000], 5, 1, 64, 64, 1.0),                   # more splits than a round of the merge
     ([100, 60], [2600, 2000], 4, 4, 64, 16, 2.0),        # tiles cut at several places
     ([300, 10, 0, 700], [2300, 1800, 5, 2000], 16, 16, 64, 16, 1.0),  # more pieces than SMs
+    ([100, 40, 0, 300], [6300, 5800, 5, 6000], 16, 16, 64, 16, 1.0),
+    ([35] * 20, [1900 + 13 * i for i in range(20)], 16, 16, 64, 32, 1.0),   # long lists that
+    ([35] * 40, [1900 + 13 * i for i in range(40)], 8, 8, 128, 16, 1.0),    # stay whole
+    ([35] * 36, [200 + 17 * i for i in range(35)] + [9000], 2, 2, 64, 16, 1.0),  # one is cut
 ])
 def test_long_caches(cp, new, kv, H, Hk, D, size, std):
     x = Batch(new, kv, H, Hk, D, size, seed=3, std=std)
