@@ -16,7 +16,17 @@
 // Softmax: p = 2^(s scale log2 e - m), one pass with a running maximum m that
 // moves only when a group's maximum exceeds it by 8 powers of two (O and l
 // share the reference, so O / l and m + ln l do not depend on it); l sums p in
-// fp32, P is rounded to bf16 for its product with V, O accumulates in fp32.
+// fp32, O accumulates in fp32.  The matrix instructions take P in bf16.  Blocks of
+// up to 16 rows (the decoding step) keep what that rounding leaves: the remainder
+// p - bf16(p) is a second bf16 operand, so P is off by 2^-16 and O has its own
+// rounding's error alone (relative to 64 bits 0.0017 instead of 0.0020).  Up to 8
+// rows leave the other half of the 16-row operand free, which takes the remainder
+// without another instruction (a token each of 64 caches, 32 / 8 heads of 128: 655
+// instead of 645 us; 65 caches of 327 to 655 keys, 4 KV heads: 22.6, before 22.9);
+// 9 to 16 rows cost a second product (the same rows in such a block: 658 and 23.7
+// us).  Blocks of 32 rows round P to bf16 as the tile kernel and the packed forward
+// do: their products take most of the time, and a second one costs an eighth of it
+// (drafts 33.2 and 37.4 us; 4 tokens of 8 heads each over 17 caches 82 and 92 us).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -53,10 +63,15 @@ __device__ __forceinline__ int at(int r, int c) {
 
 }  // namespace
 
-template <int D, int MT, bool PLAN>
+template <int D, int MT, bool HALF, bool PLAN>
 __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedParams p) {
   using C = RowsCfg<D>;
+  // HALF: at most 8 rows, which lie in the second half of the block (its rows end
+  // with the sequence's); the first half of P holds the remainders.
+  static_assert(!HALF || MT == 1);
   constexpr int kRows = 16 * MT;
+  constexpr int kH0 = HALF ? 1 : 0;
+  constexpr bool kSecond = MT == 1 && !HALF;  // the remainders are an operand of their own
   constexpr int kCh = D / 8;         // 16-byte chunks of a row
   constexpr int kRpi = 32 / kCh;     // rows one warp copy covers
   extern __shared__ __align__(128) uint8_t smem[];
@@ -230,6 +245,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            if (HALF && !(i & 2)) continue;
             const int key = key0 + (i >> 2) * 8 + 2 * (lane & 3) + (i & 1);
             if (key >= lim[mt][(i >> 1) & 1] || j >= n) s[g][mt][i >> 2][i & 3] = kNegInfR;
           }
@@ -240,7 +256,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = kH0; hf < 2; ++hf) {
         float t = kNegInfR;
 #pragma unroll
         for (int g = 0; g < NG; ++g)
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = kH0; hf < 2; ++hf) {
           const float mn = fmaxf(m[mt][hf], top[mt][hf]);
           const float alpha = m[mt][hf] == kNegInfR ? 0.f : ex2_approx(m[mt][hf] - mn);
           m[mt][hf] = mn;
@@ -264,23 +280,31 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
           for (int f = 0; f < D / 8; ++f) {
             o[mt][f][2 * hf] *= alpha;
             o[mt][f][2 * hf + 1] *= alpha;
+            if (HALF) {
+              o[mt][f][0] *= alpha;
+              o[mt][f][1] *= alpha;
+            }
           }
         }
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      uint32_t pa[MT][4];
+      uint32_t pa[MT][4], pb[4];  // P and, of up to 16 rows, what its rounding left
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = kH0; hf < 2; ++hf) {
           const float ref = m[mt][hf] == kNegInfR ? 0.f : m[mt][hf];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const float p0 = ex2_approx(fmaf(s[g][mt][t][2 * hf], p.scale_log2, -ref));
             const float p1 = ex2_approx(fmaf(s[g][mt][t][2 * hf + 1], p.scale_log2, -ref));
             l[mt][hf] += p0 + p1;
-            pa[mt][2 * t + hf] = pack_bf16x2(p0, p1);
+            const uint32_t up = pack_bf16x2(p0, p1);
+            pa[mt][2 * t + hf] = up;
+            if (MT == 1)
+              (HALF ? pa[mt][2 * t] : pb[2 * t + hf]) = pack_bf16x2(
+                  p0 - __uint_as_float(up << 16), p1 - __uint_as_float(up & 0xffff0000u));
           }
         }
 #pragma unroll
@@ -293,6 +317,10 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
         for (int mt = 0; mt < MT; ++mt) {
           mma_16816(o[mt][2 * f], pa[mt], b[0], b[1]);
           mma_16816(o[mt][2 * f + 1], pa[mt], b[2], b[3]);
+          if (kSecond) {
+            mma_16816(o[mt][2 * f], pb, b[0], b[1]);
+            mma_16816(o[mt][2 * f + 1], pb, b[2], b[3]);
+          }
         }
       }
     }
@@ -309,7 +337,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = kH0; hf < 2; ++hf) {
       const int r = mt * 16 + hf * 8 + (lane >> 2);
       float sum = l[mt][hf];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -321,7 +349,8 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
 #pragma unroll
       for (int f = 0; f < D / 8; ++f)
         *reinterpret_cast<float2*>(so + r * D + f * 8 + 2 * (lane & 3)) =
-            make_float2(o[mt][f][2 * hf], o[mt][f][2 * hf + 1]);
+            HALF ? make_float2(o[mt][f][2] + o[mt][f][0], o[mt][f][3] + o[mt][f][1])
+                 : make_float2(o[mt][f][2 * hf], o[mt][f][2 * hf + 1]);
     }
   __syncthreads();
   // Joins the warps' states: to the partial results of `to` (a slot), or to
@@ -460,9 +489,9 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   join(-1);
 }
 
-template <int D, int MT, bool PLAN>
+template <int D, int MT, bool HALF, bool PLAN>
 static cudaError_t launch_paged_rows_t(const PagedParams& p, cudaStream_t stream) {
-  auto kern = paged_rows_kernel<D, MT, PLAN>;
+  auto kern = paged_rows_kernel<D, MT, HALF, PLAN>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              RowsCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
@@ -479,13 +508,17 @@ static cudaError_t launch_paged_rows_t(const PagedParams& p, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <int D, int MT, bool HALF>
+static cudaError_t launch_paged_rows_p(const PagedParams& p, cudaStream_t stream) {
+  return p.shape.plan ? launch_paged_rows_t<D, MT, HALF, true>(p, stream)
+                      : launch_paged_rows_t<D, MT, HALF, false>(p, stream);
+}
+
 template <int D>
 static cudaError_t launch_paged_rows_d(const PagedParams& p, cudaStream_t stream) {
-  if (p.shape.rows == 16)
-    return p.shape.plan ? launch_paged_rows_t<D, 1, true>(p, stream)
-                        : launch_paged_rows_t<D, 1, false>(p, stream);
-  return p.shape.plan ? launch_paged_rows_t<D, 2, true>(p, stream)
-                      : launch_paged_rows_t<D, 2, false>(p, stream);
+  if (p.shape.rows != 16) return launch_paged_rows_p<D, 2, false>(p, stream);
+  return p.max_seqlen * p.group <= 8 ? launch_paged_rows_p<D, 1, true>(p, stream)
+                                     : launch_paged_rows_p<D, 1, false>(p, stream);
 }
 
 cudaError_t launch_paged_rows(const PagedParams& p, int D, cudaStream_t stream) {
