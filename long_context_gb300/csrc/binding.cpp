@@ -267,6 +267,8 @@ TurnArgs turn_args(PyObject* positions, PyObject* table, PyObject* wq, PyObject*
     const at::Tensor& t = tensor(table, "rope_table", at::kFloat);
     if (t.dim() != 2)
       raise(PyExc_ValueError, "rope_table must be [max_position, rotary_dim]");
+    // Its address would be null, which means that there is no rotation.
+    if (t.numel() == 0) raise(PyExc_ValueError, "rope_table must not be empty");
     a.max_pos = as_int(t.size(0), "max_position");
     a.rot = as_int(t.size(1), "rotary_dim");
     a.table = static_cast<const float*>(flat(table, "rope_table", at::kFloat, dev, t.sizes()));
