@@ -509,7 +509,8 @@ int cpattn_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride,
  * the keys with cpattn_qk_norm_rope's norm and rotation on the way, and
  * optionally the new queries, normed and rotated, to q_out.
  *   k, v, q, q_out   as cpattn_qk_norm_rope's arrays; v is copied as it is.
- *                 q may be NULL (then num_heads = 0, q_weight and q_out NULL).
+ *                 q may be NULL (then num_heads = 0, q_weight and q_out NULL;
+ *                 with total_tokens = 0 every array may be).
  *   rope_table, rotary_dim, max_position, interleaved, eps  as there; NULL: no
  *                 rotation.  k_weight (with q: both or neither) NULL: no norm.
  *   status        device int32 [1] or NULL: set to CPATTN_ERR_INVALID_ARG (else

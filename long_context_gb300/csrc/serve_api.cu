@@ -315,12 +315,14 @@ extern "C" int cpattn_paged_append(
     int32_t interleaved, const void* q_weight, const void* k_weight, float eps, const void* q,
     int64_t q_stride, int32_t num_heads, void* q_out, int64_t q_out_stride, int32_t* status,
     void* stream) {
-  int st = check_turn(rope_table, rotary_dim, max_position, q_weight, k_weight, q != nullptr, eps,
+  // Queries of no tokens may have a null address.
+  const bool with_q = q != nullptr || (total_tokens == 0 && num_heads > 0);
+  int st = check_turn(rope_table, rotary_dim, max_position, q_weight, k_weight, with_q, eps,
                       interleaved, head_dim);
   if (st != CPATTN_OK) return st;
-  if (q == nullptr && (q_weight != nullptr || q_out != nullptr || num_heads != 0))
+  if (!with_q && (q_weight != nullptr || q_out != nullptr || num_heads != 0))
     return CPATTN_ERR_INVALID_ARG;
-  if (q != nullptr && num_heads < 1) return CPATTN_ERR_INVALID_ARG;
+  if (with_q && num_heads < 1) return CPATTN_ERR_INVALID_ARG;
   if (num_kv_heads < 1 || num_heads < 0 || num_seqs < 0 ||
       !counts_ok(total_tokens, static_cast<int64_t>(num_heads) + 2 * static_cast<int64_t>(num_kv_heads)))
     return CPATTN_ERR_INVALID_ARG;

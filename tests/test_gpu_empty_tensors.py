@@ -32,3 +32,18 @@ def test_a_table_without_positions_is_no_missing_table(cp):  # noqa: F811
         with pytest.raises(refused):
             cp.paged_append(k, k, kc, vc, t, cu, kv, rope_table=empty)
     assert (out == 7).all() and torch.equal(kc.nan_to_num(9), before.nan_to_num(9))
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_of_no_tokens_with_queries(cp, norm):  # noqa: F811
+    """A step in which no sequence has a new token."""
+    x = Batch([0, 0], [5, 20], 4, 2, 64, 16, seed=12)
+    _, kc, vc, t, cu, kv = x.on_gpu()
+    qkv = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda") if norm else None
+    before = kc.clone(), vc.clone()
+    q = cp.paged_append(qkv[:, 4:6], qkv[:, 6:], kc, vc, t, cu, kv, rope_table=table(32, 64).cuda(),
+                        k_weight=w, q=qkv[:, :4], q_weight=w)
+    assert q.shape == (0, 4, 64)
+    for a, b in zip((kc, vc), before):
+        assert torch.equal(a.nan_to_num(9), b.nan_to_num(9))
