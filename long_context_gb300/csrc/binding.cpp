@@ -150,20 +150,24 @@ class Call {
  public:
   Call(c10::Device dev, PyObject* stream) : dev_(dev), guard_(dev) {
     const auto current = c10::cuda::getCurrentCUDAStream(dev.index());
-    stream_ = current.unwrap();
+    current_ = stream_ = current.unwrap();
     if (stream != Py_None) {
       const int64_t id = attr(stream, "stream_id"), index = attr(stream, "device_index");
       if (index != dev.index())
         raise(PyExc_ValueError, "stream must be on " + dev.str() + ", got cuda:" +
                                     std::to_string(index));
       stream_ = c10::Stream::unpack3(id, dev.index(), c10::DeviceType::CUDA);
-      other_ = stream_ != current.unwrap();
+      other_ = stream_ != current_;
     }
   }
+  // Memory of the call's stream: a block of the current one's may still have work
+  // pending there.  The caller reads the tensor on the current stream, which the
+  // allocator has to be told.
   at::Tensor make(c10::IntArrayRef shape, c10::ScalarType dtype) {
+    if (!other_) return at::detail::empty_cuda(shape, dtype, dev_, std::nullopt);
+    const c10::cuda::CUDAStreamGuard on(stream_);
     at::Tensor t = at::detail::empty_cuda(shape, dtype, dev_, std::nullopt);
-    // On a stream that is not current the allocator has to be told who uses it.
-    if (other_) t.record_stream(stream_);
+    t.record_stream(current_);
     return t;
   }
   void* stream() const { return c10::cuda::CUDAStream(stream_).stream(); }
@@ -189,6 +193,7 @@ class Call {
   c10::Device dev_;
   c10::cuda::CUDAGuard guard_;
   c10::Stream stream_{c10::Stream::DEFAULT, c10::Device(c10::DeviceType::CPU)};
+  c10::Stream current_{c10::Stream::DEFAULT, c10::Device(c10::DeviceType::CPU)};
   bool other_ = false;
 };
 
