@@ -25,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcpattn.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding.for")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 SOURCES = ["plan.cpp", "api.cu", "schedule.cu", "merge.cu", "attn_fwd.cu", "attn_bwd.cu",
@@ -112,7 +113,19 @@ def _run(cmd, what):
 
 def _torch_dir():
     import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else None
+
+
+def _binding_for():
+    """What ``_binding.so`` is bound to -- the Python and the PyTorch that load it --
+    or None where no PyTorch with CUDA is installed: then there is no binding, and
+    the calls that need it say so."""
+    root = _torch_dir()
+    if root is None or not os.path.exists(os.path.join(root, "lib", "libc10_cuda.so")):
+        return None
+    with open(os.path.join(root, "version.py")) as f:
+        return "%s\n%s\n%s" % (sys.version, root, f.read())
 
 
 def _compile_binding():
@@ -134,21 +147,29 @@ def _link_binding(obj):
           "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
           "-ltorch", "-lc10_cuda", "-lc10"], "linking _binding.so")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_for())
 
 
 def _binding_stale():
-    if not os.path.exists(BINDING):
+    want = _binding_for()
+    if want is None:
+        return False
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_FOR):
         return True
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "cpattn.h"), os.path.abspath(__file__),
-            os.path.join(_torch_dir(), "version.py")]
+    with open(BINDING_FOR) as f:
+        if f.read() != want:
+            return True
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "cpattn.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps)
 
 
 def build(force=False, verbose_ptxas=False, quiet=True):
-    """Compile and link ``libcpattn.so`` and ``_binding.so`` unless they are up
-    to date."""
+    """Compile and link ``libcpattn.so`` and, where PyTorch with CUDA is installed,
+    ``_binding.so`` unless they are up to date.  The library does not depend on the
+    binding: an error of the latter is raised when the former is in place."""
     os.makedirs(BUILD, exist_ok=True)
-    binding = force or _binding_stale()
+    binding = _binding_for() is not None and (force or _binding_stale())
     if not force and not _stale():
         if binding:
             _link_binding(_compile_binding())
@@ -167,7 +188,6 @@ def build(force=False, verbose_ptxas=False, quiet=True):
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         obj = ex.submit(_compile_binding) if binding else None
         results = list(ex.map(compile_one, SOURCES))
-        obj = obj and obj.result()
     if not quiet or verbose_ptxas:
         for _, log in results:
             if log.strip():
@@ -180,7 +200,7 @@ def build(force=False, verbose_ptxas=False, quiet=True):
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
     if binding:
-        _link_binding(obj)
+        _link_binding(obj.result())
     return LIB
 
 

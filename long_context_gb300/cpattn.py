@@ -4,8 +4,9 @@ Argument marshalling only: tensors are checked for dtype, device, layout and
 contiguity, then their device pointers are handed to ``libcpattn.so`` together
 with PyTorch's current CUDA stream.  Every step of the computation runs in the
 library's kernels; there is no fallback.  Importing this module raises
-``ImportError`` when the library (or the compiled part of this binding,
-``_binding.so``) has not been built (``build.build()``).
+``ImportError`` when the library has not been built (``build.build()``); so does
+the first of the per-layer calls when the compiled part of this binding that
+they need, ``_binding.so``, is missing or made for another PyTorch.
 """
 
 from __future__ import annotations
@@ -24,11 +25,6 @@ if not os.path.exists(_LIB_PATH):
         "libcpattn.so is missing at %s; build it with "
         "long_context_gb300.build.build()" % _LIB_PATH)
 _lib = ctypes.CDLL(_LIB_PATH)
-try:
-    from . import _binding
-except ImportError as e:
-    raise ImportError("_binding.so is missing or does not match this PyTorch; build it with "
-                      "long_context_gb300.build.build()") from e
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -122,9 +118,6 @@ class CpattnError(RuntimeError):
     def __init__(self, status, what):
         self.status = status
         super().__init__("%s: %s (status %d)" % (what, status_string(status), status))
-
-
-_binding.set_error(CpattnError)
 
 
 # ---------------------------------------------------------------- tracing --
@@ -740,7 +733,23 @@ def merge(o_steps, m_steps, l_steps, *, out_o=None, out_m=None, out_l=None, stre
 
 # ------------------------------------------------- norm + rotation, paged cache --
 # These calls run once per layer of a decoding step, where the host's time
-# counts: ``_binding`` (csrc/binding.cpp) checks and marshals their arguments.
+# counts: ``_binding`` (csrc/binding.cpp) checks and marshals their arguments.  It is
+# bound to the PyTorch that it was built against, so only they load it.
+_compiled = None
+
+
+def _binding():
+    global _compiled
+    if _compiled is None:
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("_binding.so is missing or does not match this PyTorch; build it "
+                              "with long_context_gb300.build.build()") from e
+        module.set_error(CpattnError)
+        _compiled = module
+    return _compiled
+
 
 @_traced("cpattn_qk_norm_rope")
 def qk_norm_rope(q, k, positions, rope_table, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -756,8 +765,8 @@ def qk_norm_rope(q, k, positions, rope_table, *, q_weight=None, k_weight=None, e
     may be ``q`` and ``k_out`` may be ``k``.  ``status``: int32 ``[1]``, set
     when a position is outside the table (its rows are left as they were).
     """
-    return _binding.qk_norm_rope(q, k, positions, rope_table, q_weight, k_weight, eps, interleaved,
-                                 q_out, k_out, status, stream)
+    return _binding().qk_norm_rope(q, k, positions, rope_table, q_weight, k_weight, eps,
+                                   interleaved, q_out, k_out, status, stream)
 
 
 @_traced("cpattn_qk_norm_rope_bwd")
@@ -771,9 +780,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, rope_table, *, q_weight=No
     ``dq_out``, ``dk_out``: the gradients of its outputs (token strides as the
     inputs'); the other arguments as in the call being differentiated.
     """
-    return _binding.qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, rope_table, q_weight, k_weight,
-                                     eps, interleaved, dq, dk, dq_weight, dk_weight, workspace,
-                                     status, stream)
+    return _binding().qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, rope_table, q_weight,
+                                       k_weight, eps, interleaved, dq, dk, dq_weight, dk_weight,
+                                       workspace, status, stream)
 
 
 @_traced("cpattn_paged_append")
@@ -790,8 +799,9 @@ def paged_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, rop
     ``[num_pages, page_size, Hk, D]``; ``page_table [B, max_pages]``: int32.
     ``status``: int32 ``[1]``, set when a token could not be placed.
     """
-    return _binding.paged_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, rope_table,
-                                 interleaved, k_weight, eps, q, q_weight, q_out, status, stream)
+    return _binding().paged_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens,
+                                   rope_table, interleaved, k_weight, eps, q, q_weight, q_out,
+                                   status, stream)
 
 
 def paged_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen):
@@ -822,8 +832,8 @@ def paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, max_seql
     sequence's new tokens and cache length.  Rows behind ``cu_seqlens[B]`` are
     not written.
     """
-    return _binding.paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, max_seqlen,
-                               max_kv_len, softmax_scale, causal, out, lse, workspace, stream)
+    return _binding().paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, max_seqlen,
+                                 max_kv_len, softmax_scale, causal, out, lse, workspace, stream)
 
 
 def poll_error(workspace, stream=None):
