@@ -90,9 +90,10 @@ def _build_variant(name, define, force):
 
 def build_fault_injection(force=False):
     """Test-only variant ``libcpattn_fault.so`` built with
-    ``-DCPATTN_FAULT_INJECT_DROP_P``: the attention kernel's first CTA skips
-    one hand-off so that a bounded device wait runs out.  Used by the failure
-    detection test; never loaded by the package."""
+    ``-DCPATTN_FAULT_INJECT_DROP_P``: the first CTA of the attention kernels
+    (forward, backward, paged tiles) skips one hand-off so that a bounded device
+    wait runs out.  Used by the failure detection tests; never loaded by the
+    package."""
     return _build_variant("cpattn_fault", "CPATTN_FAULT_INJECT_DROP_P", force)
 
 

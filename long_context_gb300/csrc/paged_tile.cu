@@ -115,8 +115,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int err0 = __ldcg(&p.hdr->error);
   const int4* wp = reinterpret_cast<const int4*>(p.work + e);
   const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1);
-  // After one CTA gave up on a wait, the rest of the grid does no work.
-  if (e >= n_work || err0 == kErrTimeoutT) return;
+  if (e >= n_work) return;
+  // After one CTA gave up on a wait, the rest of the grid does no work.  The CTA
+  // goes by one answer: the word may change between its threads' reads, and a warp
+  // that stayed would wait at a named barrier, without limit, for one that left.
+  if (__syncthreads_or(err0 == kErrTimeoutT)) return;
   const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
   const int kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
   const int G = p.group;
@@ -551,7 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(s_addr + 32, pk + 32);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[t]);
+#ifdef CPATTN_FAULT_INJECT_DROP_P
+        // Test-only build: CTA 0 never hands its first P tile of Q tile 0 to the
+        // MMA warp, whose bounded wait then runs out (no trap, no fault).
+        if (!(blockIdx.x == 0 && t == 0 && x == 0))
+#endif
+          mbar_arrive(&p_full[t]);
       }
       if (ok && n > 0) {
         ok = __all_sync(0xffffffffu,
