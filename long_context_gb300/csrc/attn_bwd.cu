@@ -405,7 +405,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int err0 = __ldcg(&p.hdr->error);
   const CtaWork work = __ldg(&p.table[x_cta]);
   if (x_cta >= n_ctas) return;
-  if (err0 == kErrTimeout) return;
 
   const UnitIds u = decode(work);
   const int kv0 = min(u.rank * u.chunk, u.L) + u.blk * kT;        // first key of the tile
@@ -474,8 +473,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(says_timeout(err0));
   tc_fence_after();
+  if (gave_up) {
+    if (warp == 8 && lane == 0) {  // the copies above must land before exit
+      wait_drain(a_full, 0);
+      Walk<KRing> w;
+      w.start(ring);
+      if (!w.done(ring)) {
+        wait_drain(&b0_full[0], 0);
+        wait_drain(&b1_full[0], 0);
+      }
+    }
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(*tmem_slot, C::kTmemCols);
+    return;
+  }
 
   static_assert(kBwdSoftmaxRegs == 224 && kBwdCtrlRegs == 56, "immediates below");
   if (warp >= 8) {
@@ -830,7 +843,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // Programmatic dependent of the dK/dV kernel, which it does not read: it
   // starts while dK/dV's last CTAs run, and every CTA waits for dK/dV before
   // it exits, so the backward completes only when both have.
-  if (x_cta >= n_ctas || err0 == kErrTimeout) {
+  if (x_cta >= n_ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
@@ -903,8 +916,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(says_timeout(err0));
   tc_fence_after();
+  if (gave_up) {
+    if (warp == 8 && lane == 0) {  // the copies above must land before exit
+      wait_drain(a_full, 0);
+      Walk<QRing> w;
+      w.start(ring);
+      if (!w.done(ring)) {
+        wait_drain(&b0_full[0], 0);
+        wait_drain(&b1_full[0], 0);
+      }
+    }
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(*tmem_slot, C::kTmemCols);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   static_assert(kBwdSoftmaxRegs == 224 && kBwdCtrlRegs == 56, "immediates below");
   if (warp >= 8) {

@@ -166,8 +166,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int err0 = __ldcg(&p.hdr->error);
   const CtaWork work = __ldg(&p.table[x_cta]);
   if (x_cta >= n_ctas) return;
-  // After one CTA gave up on a wait, the rest of the grid does no work.
-  if (err0 == kErrTimeout) return;
 
   // CTA -> (sample, head, rank, block): see work.cuh for the order.
   SampleGeom geo;
@@ -286,9 +284,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(says_timeout(err0));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (A barrier before the setup instead cost 1 % of the packed 16K step.)
+  if (gave_up) {
+    if (warp == 8 && lane == 0) {  // the copies above must land before exit
+      wait_drain(q_full, 0);
+      Cursor cur;
+      cur.start(ring);
+      if (cur.s < ring.num_steps) {
+        wait_drain(&k_full[0], 0);
+        wait_drain(&v_full[0], 0);
+      }
+    }
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, C::kTmemCols);
+    return;
+  }
   static_assert(kSoftmaxRegs == 224 && kCtrlRegs == 56, "immediates below");
 
   if (warp >= 8) {

@@ -116,10 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int4* wp = reinterpret_cast<const int4*>(p.work + e);
   const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1);
   if (e >= n_work) return;
-  // After one CTA gave up on a wait, the rest of the grid does no work.  The CTA
-  // goes by one answer: the word may change between its threads' reads, and a warp
-  // that stayed would wait at a named barrier, without limit, for one that left.
-  if (__syncthreads_or(err0 == kErrTimeoutT)) return;
+  if (__syncthreads_or(says_timeout(err0))) return;
   const int tok0 = w0.x, q_len = w0.y, kv_len = w0.z, seq = w0.w;
   const int kv_lo = w1.y, kv_hi = w1.z, slot = w1.w;
   const int G = p.group;

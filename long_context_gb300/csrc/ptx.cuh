@@ -75,6 +75,18 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t pari
 
 // Give up after this long: no legitimate wait inside one CTA comes close.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+// Whether the workspace's error word says that a CTA gave up on a wait: the rest of
+// the grid then does no work.  The word may change between two threads' reads, and
+// a warp that stayed would wait at a named barrier, without limit, for one that
+// left, so a CTA leaves by __syncthreads_or of this.  (In the test-only build one
+// thread of CTA 1 reads it so, the others do not.)
+__device__ __forceinline__ bool says_timeout(int error) {
+#ifdef CPATTN_FAULT_INJECT_DROP_P
+  if (blockIdx.x == 1 && threadIdx.x == blockDim.x - 1) return true;
+#endif
+  return error == 6;  // CPATTN_ERR_DEVICE_TIMEOUT
+}
+
 // Longest single sleep inside wait_bounded (bounds how late an abort raised
 // by another warp is seen).
 constexpr uint32_t kWaitSleepNs = 20000;  // 20 us
