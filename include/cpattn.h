@@ -543,7 +543,8 @@ int cpattn_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride,
  * multiplies its value.
  * Precision: fp32 scores, softmax and sums; P is rounded to bf16 for its
  * product with V (with max_seqlen * H / num_kv_heads <= 16, the decoding step, P
- * keeps 16 bits); one rounding of O to bf16.  Sums are taken in a fixed order.
+ * keeps 16 bits); one rounding of O to bf16.  Sums are taken in a fixed order:
+ * equal inputs under equal bounds give equal bits.
  * Both calls enqueue on `stream`, read all lengths on the device (a captured
  * call can be replayed with other lengths within its bounds), and return
  * argument errors before any launch.

@@ -10,7 +10,8 @@
 // Tiles (one CTA a SM, an item is up to hundreds of units): left whole, the items
 // go to the SMs by decreasing size, and the last SM is done after about
 //   E = max over k of (k + 1) p[k SMs],  p the sizes in decreasing order from p[0]
-// (k + 1 items as large as p[k SMs] meet on some SM).  Cut, every SM has
+// (k + 1 items as large as p[k SMs] meet on some SM; sorted by counting, so p is
+// the lower edge of one of 128 ranges of sizes for k > 0).  Cut, every SM has
 // C = W heads / SMs units and the merge and the pieces' starts to pay, about
 // `keep` = 14 units; so the items are cut when 65 / 64 E > C + 14.  (D = 128, us
 // uncut and cut: C 458, E 544: 829 and 745; C 188, E 200: 359 and 341; C 1.5, E 16:
@@ -23,9 +24,11 @@
 //
 // Either way the split items have at most 2 ctas / heads splits in all (an item
 // of n > 1 splits has more than (n - 1) target units, or n - 1 cuts), which
-// bounds the partial results' memory on the host.  Which items are cut, and
-// where, depends on the lengths alone; only the order of equally large splits
-// in the list is left to chance, and no result depends on it.
+// bounds the partial results' memory on the host.  The host's bounds
+// choose the blocks' rows (PagedShape); which items are then cut, and where,
+// depends on the lengths and the number of heads alone, whichever kernel below
+// lists them.  Only the order of the list differs between the kernels and, for
+// equally large splits, between runs, and no result depends on it.
 //
 // The merge joins an item's normalised partials: LSE = ln sum exp(lse_s),
 // O = sum exp(lse_s - LSE) O_s.
@@ -123,16 +126,20 @@ __device__ __forceinline__ int item_units(const PagedParams& p, const PagedItem&
 }
 
 // Which of kBuckets equal ranges of [0, largest] holds `units` (below 2^24, as
-// units of 128 keys are).
+// units of 128 keys are), and where a range begins.
 __device__ __forceinline__ int size_bucket(int units, int largest) {
   return min(kBuckets - 1, static_cast<int>(static_cast<unsigned>(units) * kBuckets /
                                             (static_cast<unsigned>(largest) + 1)));
+}
+__device__ __forceinline__ int bucket_edge(int bucket, int largest) {
+  return static_cast<int>(static_cast<unsigned>(bucket) *
+                          (static_cast<unsigned>(largest) + 1) / kBuckets);
 }
 
 }  // namespace
 
 // Tiles, at most 32 items: every warp works the list out in its lanes, an item
-// each, and the warps share the writing.  Same cuts and order as below.  (Three
+// each, and the warps share the writing.  Same cuts as below.  (Three
 // sequences of 90 to 193 tokens 16.6 -> 14.4 us, five of 10 to 16 16.5 -> 12.4 us.)
 __global__ void __launch_bounds__(128) paged_schedule_few_kernel(const PagedParams p) {
   __shared__ int s_cost[256];
@@ -209,10 +216,11 @@ __global__ void __launch_bounds__(128) paged_schedule_few_kernel(const PagedPara
       rank += u > units || (u == units && o < lane);
     }
     // This item's bound of the uncut time, if its rank gives one.
-    int uncut = 0;
+    int uncut = have && rank == 0 ? units : 0;
+    const int edge = bucket_edge(size_bucket(units, top), top);
 #pragma unroll
-    for (int k = 0; k <= kMeet; ++k)
-      if (have && rank == k * p.shape.ctas / p.num_kv_heads) uncut = (k + 1) * units;
+    for (int k = 1; k <= kMeet; ++k)
+      if (have && rank == k * p.shape.ctas / p.num_kv_heads) uncut = max(uncut, (k + 1) * edge);
     uncut = __reduce_max_sync(0xffffffffu, uncut);
     cutting = paged_cut(p.shape, all, p.num_kv_heads, uncut);
   }
@@ -368,9 +376,8 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
     const int upto = static_cast<int>(ps_scan<NT>(mine, warp_sums));
     for (int k = 1; k <= kMeet; ++k) {
       const int rank = k * p.shape.ctas / p.num_kv_heads;
-      const unsigned size = (kBuckets - 1u - tid) * (top + 1u) / kBuckets;
       if (upto - mine <= rank && rank < upto)
-        atomicMax(&s_top, (k + 1) * static_cast<int>(size));
+        atomicMax(&s_top, (k + 1) * bucket_edge(kBuckets - 1 - tid, top));
     }
     __syncthreads();
     cutting = paged_cut(p.shape, all, p.num_kv_heads, s_top);
