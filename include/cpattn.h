@@ -502,7 +502,9 @@ int cpattn_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride,
  * cache, the new ones among them; cu_seqlens [num_seqs + 1] packs the new
  * tokens, so new token i of the q_len of sequence b stands at position
  * kv_lens[b] - q_len + i.  cu_seqlens[num_seqs] may be below the token count of
- * the arrays: the rows behind the last sequence are neither read nor written.
+ * the arrays: the rows behind the last sequence are not written, and what they
+ * hold does not matter (cpattn_paged_append reads them, to no effect;
+ * cpattn_paged_attn does not).
  * The source pages have no counterpart to these two calls.
  *
  * cpattn_paged_append -- writes the new tokens' keys and values into the cache,
