@@ -56,6 +56,9 @@ int page_shift_of(int32_t page_size) {
   return -1;
 }
 
+// The shares are those of a GB300's 152 SMs, not of the device at hand, because the
+// workspace's size follows from them and is asked for without a device; on a part
+// with fewer only the balance would suffer.
 PagedShape paged_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   PagedShape s;
   const int64_t rows = group * max_seqlen;
