@@ -534,8 +534,9 @@ int cpattn_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride,
  *                 kv_lens; they choose the kernel and size its grid.
  *   out           bf16 [total_q, H, D] (not q);  lse float [total_q, H] or NULL.
  *   workspace     >= cpattn_paged_attn_workspace_size(...) bytes, 256-byte
- *                 aligned; its first bytes hold the error word.  Calls that
- *                 may overlap need workspaces of their own.
+ *                 aligned; its first bytes hold the error word.  One made for a
+ *                 batch does for smaller ones (total_q, num_seqs, max_seqlen) of the
+ *                 same heads.  Calls that may overlap need workspaces of their own.
  * The kernels check cu_seqlens, kv_lens (0 .. max_kv_len and max_pages *
  * page_size) and the bounds; a violation sets CPATTN_ERR_INVALID_ARG in the
  * error word (cpattn_poll_error) and writes no output.  A page number outside

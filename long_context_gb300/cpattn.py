@@ -814,7 +814,8 @@ def paged_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, m
 
 def alloc_paged_workspace(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
                           device=None):
-    """A device workspace sized for :func:`paged_attn` (torch-owned)."""
+    """A device workspace sized for :func:`paged_attn` (torch-owned), for this batch
+    and smaller ones of the same heads."""
     n = paged_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 

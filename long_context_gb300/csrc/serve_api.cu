@@ -2,6 +2,7 @@
 // include/cpattn.h): argument checks, workspace layout and kernel launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -137,6 +138,22 @@ PagedLayout paged_layout(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int3
   off = serve_align(off + rows * sizeof(float));
   l.total = off;
   return l;
+}
+
+// Bytes for this batch and every smaller one (fewer tokens, sequences or new tokens
+// of a sequence): the largest layout of the shapes among them, which change at 16
+// and at 32 rows and at kPlanSeqs sequences.
+size_t paged_workspace(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t D,
+                       int32_t max_seqlen) {
+  const int64_t group = H / Hk;
+  size_t most = 0;
+  for (const int64_t rows : {int64_t(16), int64_t(32), group * max_seqlen}) {
+    const int32_t len = static_cast<int32_t>(std::min<int64_t>(max_seqlen, rows / group));
+    for (const int32_t seqs : {B, std::min(B, kPlanSeqs)})
+      most = std::max(
+          most, paged_layout(total_q, seqs, H, Hk, D, paged_shape(group, len, seqs)).total);
+  }
+  return most;
 }
 
 bool paged_sizes_ok(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t max_seqlen) {
@@ -394,9 +411,7 @@ extern "C" size_t cpattn_paged_attn_workspace_size(int64_t total_q, int32_t num_
   if (!paged_sizes_ok(total_q, num_seqs, num_heads, num_kv_heads, max_seqlen) ||
       (head_dim != 64 && head_dim != 128) || num_heads / num_kv_heads > kPagedMaxGroup)
     return 0;
-  return paged_layout(total_q, num_seqs, num_heads, num_kv_heads, head_dim,
-                      paged_shape(num_heads / num_kv_heads, max_seqlen, num_seqs))
-      .total;
+  return paged_workspace(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen);
 }
 
 extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,

@@ -94,3 +94,20 @@ def test_a_bad_page_in_a_split(cp, most, H, Hk, D):  # noqa: F811
         got = cp.paged_attn(q, kc, vc, t, cu, kvl, workspace=ws, **x.bounds())
         assert cp.poll_error(ws) == cp.OK
         assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+
+
+def test_one_workspace_while_sequences_finish(cp):  # noqa: F811
+    """Made for the first step of 34 sequences of up to 40 new tokens, used by every
+    later and smaller one."""
+    H, Hk, D = 8, 2, 64
+    x = Batch([1] * 34, [40 + 61 * i for i in range(34)], H, Hk, D, 16, seed=47)
+    q, kc, vc, t, cu, kv = x.on_gpu()
+    ws = cp.alloc_paged_workspace(34 * 40, 34, H, Hk, D, 40)
+    for n in (34, 33, 32, 31, 7, 1):
+        for bound in (40, 8, 4, 1):
+            args = (q[:n], kc, vc, t[:n], cu[:n + 1], kv[:n])
+            bounds = dict(max_seqlen=bound, max_kv_len=max(x.kv))
+            got = cp.paged_attn(*args, workspace=ws, **bounds)
+            assert cp.poll_error(ws) == cp.OK
+            want = cp.paged_attn(*args, **bounds)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
