@@ -520,7 +520,8 @@ int cpattn_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride,
  *                 (kv_lens above max_pages * page_size or below its new tokens),
  *                 its page number is outside [0, num_pages) or its position is
  *                 outside the table; such a token is left out.
- *   Two tokens with one place in the cache leave one of them there.
+ *   Two tokens with one place in the cache (sequences that share a page behind
+ *   their common tokens) leave parts of either there.
  *
  * cpattn_paged_attn -- attention of the new tokens over the cache, their own
  * keys and values in it:
