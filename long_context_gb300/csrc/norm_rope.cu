@@ -469,16 +469,20 @@ static cudaError_t launch_norm_rope_d(const NormRopeParams& p, bool interleaved,
     return p.total_tokens * (uq + (p.page_table != nullptr ? 2 : 1) * uk);
   };
   // Eight heads a lane group share a position's angles and have four times the
-  // loads in flight of two (16,384 tokens of 64 heads: 87 us, four heads 103 us,
-  // sixteen 92 us), as long as they leave every SM several rounds of CTAs (a
-  // decoding step wants its few rows spread out, 32 tokens of 40 heads: two heads
-  // 4.8 us, four 6.1 us) and at most half of their places go unused (32,768
-  // tokens of 3 + 1 heads, three quarters: 24.7 us, in runs of four 18.5 us; of
-  // 5 + 5 heads, three eighths: 18.6 us, in runs of two 24.7 us).
+  // loads in flight of two (16,384 tokens of 32 + 32 heads of 128: 85 us, four heads
+  // 95 us, two 128 us), as long as they leave every SM several rounds of CTAs (a
+  // decoding step wants its few rows spread out, 32 tokens of 32 + 8 heads of 128:
+  // two heads 4.8 us, four 6.1 us) and not too many of their places go unused, as
+  // those are computed too.  Less than half may in runs of eight, half in runs of
+  // four (32,768 tokens, heads of 128 / 64, us in runs of eight, four and two: 5 + 5
+  // heads, three eighths unused, 36.9, 43.0, 47.1 / 20.5, 24.6, 25.4; 4 + 4, half and
+  // none, 34.7, 28.6, 33.0 / 18.5, 14.7, 18.5; 3 + 1, three quarters and half, 30.8,
+  // 22.6, 24.6 / 16.5, 12.4, 13.7).
   const long long many = 12LL * num_sms * (kNrThreads / (D / 8));
   if (units_at(1) == 0) return cudaSuccess;
   auto fits = [&](int run) {
-    return units_at(run) >= many && units_at(run) * run <= 2 * units_at(1);
+    const long long places = units_at(run) * run, most = 2 * units_at(1);
+    return units_at(run) >= many && (run > 2 * kUnit ? places < most : places <= most);
   };
   if (fits(4 * kUnit))
     return launch_norm_rope_t<D, 4>(p, interleaved, units_at(4 * kUnit), stream);
