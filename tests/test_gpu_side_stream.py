@@ -67,3 +67,31 @@ def test_freed_while_the_current_stream_reads(cp):  # noqa: F811
             torch.empty_like(copy).fill_(7.0)
     torch.cuda.synchronize()
     assert torch.equal(copy.cpu(), want)
+
+
+def test_a_branch_of_a_captured_graph(cp):  # noqa: F811
+    """The calls on a stream forked inside a capture, then replayed."""
+    want = [f() for f in _calls(cp, None)]
+    s = torch.cuda.Stream()
+    calls = _calls(cp, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = [f() for f in calls]
+        torch.cuda.current_stream().wait_stream(s)
+        copies = [[o.clone() for o in r] for r in got]
+    for _ in range(2):
+        for r in copies:
+            for o in r:
+                o.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    # The first replay appends; the attention of the second reads what it wrote.
+    for r, w in zip(copies[1:], want[1:]):
+        for a, b in zip(r, w):
+            assert torch.equal(a, b)
+    again = _calls(cp, None)
+    again[3]()
+    for a, b in zip(copies[0], again[0]()):
+        assert torch.equal(a, b)
