@@ -580,6 +580,97 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
                       size_t workspace_bytes, void* stream);
 
 /*
+ * Paged KV cache in 4 bits.  A cached feature stands for c * s * u: c a 4-bit float
+ * (e2m1: 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), s the 8-bit float (e4m3,
+ * 2^-9 .. 448) of its 16 features of that token and head, u the cache's k_scale or
+ * v_scale.  k_scale and v_scale are powers of two from 2^-32 to 2^32 (1 does for
+ * most; another moves the range of s, and has to be the same in every call on the
+ * cache), so a feature's value is exact in bf16.  4.5 bits a feature; of normally
+ * distributed features the cache keeps all but 9.5 % (RMS).
+ *
+ * Pages, page_table, kv_lens and cu_seqlens are those of the bf16 cache above, but
+ * k_cache and v_cache are bytes [num_pages, num_kv_heads, page_size * 9 D / 16],
+ * 16-byte aligned, a page contiguous and page_stride BYTES from page to page (a
+ * multiple of 16).  A page of one head is page_size / 16 tiles of 9 D bytes, tile i
+ * for its tokens 16 i .. 16 i + 15.  In a tile:
+ *   for each group j of 16 features a strip of 128 bytes at 128 j: token r of the
+ *   tile has its 8 bytes at 16 ((r / 2) ^ (128 j / D)) + 8 (r % 2), features 16 j +
+ *   2 i (low half) and 16 j + 2 i + 1 (high half) in byte i, each as sign, two bits
+ *   of exponent, one of mantissa;
+ *   at 8 D + 16 j + r the scale of group j of token r.
+ * Memory that no token was written to may hold anything.
+ * The source pages have no counterpart to these calls.
+ *
+ * cpattn_paged_append_fp4 -- quantises the new tokens' keys and values into the
+ * cache (rotate the keys before: cpattn_qk_norm_rope):
+ *   s = the e4m3 nearest to max |x| / (6 u), at least 2^-9 and at most 448,
+ *   c = the e2m1 nearest to x / (s u), at most 6 in magnitude; halves to even.
+ * The bytes are those of exact arithmetic.  A group with a NaN or an infinity gets
+ * s = NaN and reads back as NaNs.  A zero has no sign.
+ *   k, v, status, and what becomes of a token without a place or of two with one
+ *   place: as cpattn_paged_append.
+ *
+ * cpattn_paged_gather_fp4 -- reads the same tokens back, the last cu_seqlens[b + 1]
+ * - cu_seqlens[b] of each sequence's kv_lens[b] (all of them, where that is
+ * kv_lens[b]): k_out, v_out bf16 [T, num_kv_heads, D] with token strides as
+ * cpattn_paged_append's inputs, exactly the cached values.  Packed keys and values
+ * as cpattn_fwd, cpattn_decode and cpattn_paged_append take them.
+ *   status        as there; rows of a token without a place, and the rows behind the
+ *                 last sequence, are left as they were.
+ *
+ * cpattn_paged_attn_fp4 -- cpattn_paged_attn over the 4-bit cache: same queries,
+ * lengths, bounds, masks, outputs, error word and limits.
+ *   workspace     >= cpattn_paged_attn_fp4_workspace_size(...) bytes, 256-byte
+ *                 aligned; one made for a batch does for smaller ones (total_q,
+ *                 num_seqs, max_seqlen, max_kv_len) of the same heads.  With more than
+ *                 128 rows of a KV head (max_seqlen * H / num_kv_heads) it holds the
+ *                 batch's caches in bf16 (num_seqs * max_kv_len * num_kv_heads * 4 D
+ *                 bytes), which the call reads them into first.
+ *   softmax_scale * k_scale has to be a normal float.
+ * num_seqs * (max_kv_len / 128 + 1) < 2^31.
+ * Precision: fp32 scores, softmax and sums over exact keys and values.  Up to 128 rows
+ * of a KV head the queries are fp16 times a power of two per row (exact down to 2^-28
+ * of the row's largest) and P is rounded to fp16; with more rows as cpattn_paged_attn.
+ * One rounding of O to bf16.  Sums are taken in a fixed order: equal inputs under
+ * equal bounds give equal bits.
+ * All three enqueue on `stream`, read all lengths on the device, and return argument
+ * errors before any launch.
+ */
+int cpattn_paged_append_fp4(const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, void* k_cache, void* v_cache,
+                            int64_t num_pages, int32_t page_size,
+                            int64_t page_stride, const int32_t* page_table,
+                            int32_t max_pages, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, int32_t num_seqs,
+                            int64_t total_tokens, int32_t num_kv_heads,
+                            int32_t head_dim, float k_scale, float v_scale,
+                            int32_t* status, void* stream);
+int cpattn_paged_gather_fp4(const void* k_cache, const void* v_cache,
+                            int64_t num_pages, int32_t page_size,
+                            int64_t page_stride, const int32_t* page_table,
+                            int32_t max_pages, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, int32_t num_seqs,
+                            int64_t total_tokens, int32_t num_kv_heads,
+                            int32_t head_dim, float k_scale, float v_scale,
+                            void* k_out, int64_t k_stride, void* v_out,
+                            int64_t v_stride, int32_t* status, void* stream);
+size_t cpattn_paged_attn_fp4_workspace_size(int64_t total_q, int32_t num_seqs,
+                                            int32_t num_heads,
+                                            int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_seqlen,
+                                            int32_t max_kv_len);
+int cpattn_paged_attn_fp4(const void* q, const void* k_cache, const void* v_cache,
+                          int64_t num_pages, int32_t page_size, int64_t page_stride,
+                          const int32_t* page_table, int32_t max_pages,
+                          const int32_t* cu_seqlens, const int32_t* kv_lens,
+                          int32_t num_seqs, int64_t total_q, int32_t max_seqlen,
+                          int32_t max_kv_len, int32_t num_heads,
+                          int32_t num_kv_heads, int32_t head_dim, float k_scale,
+                          float v_scale, float softmax_scale, int32_t causal,
+                          void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * cpattn_poll_error -- synchronise `stream` and return the workspace's error
  * word (CPATTN_OK when every kernel since the last cpattn_fwd on this
  * workspace finished normally), or CPATTN_ERR_CUDA if the stream reports a

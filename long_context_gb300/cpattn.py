@@ -106,6 +106,20 @@ _lib.cpattn_paged_attn.argtypes = [_vp, _vp, _vp, _i64, _i32, _i64, _vp, _i32, _
                                    _i64, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp,
                                    ctypes.c_size_t, _vp]
 _lib.cpattn_paged_attn.restype = ctypes.c_int
+_lib.cpattn_paged_append_fp4.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp,
+                                         _i32, _vp, _vp, _i32, _i64, _i32, _i32, _f32, _f32, _vp,
+                                         _vp]
+_lib.cpattn_paged_append_fp4.restype = ctypes.c_int
+_lib.cpattn_paged_gather_fp4.argtypes = [_vp, _vp, _i64, _i32, _i64, _vp, _i32, _vp, _vp, _i32,
+                                         _i64, _i32, _i32, _f32, _f32, _vp, _i64, _vp, _i64, _vp,
+                                         _vp]
+_lib.cpattn_paged_gather_fp4.restype = ctypes.c_int
+_lib.cpattn_paged_attn_fp4_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32, _i32]
+_lib.cpattn_paged_attn_fp4_workspace_size.restype = ctypes.c_size_t
+_lib.cpattn_paged_attn_fp4.argtypes = [_vp, _vp, _vp, _i64, _i32, _i64, _vp, _i32, _vp, _vp, _i32,
+                                       _i64, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _f32, _i32,
+                                       _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.cpattn_paged_attn_fp4.restype = ctypes.c_int
 _lib.cpattn_poll_error.argtypes = [_vp, _vp]
 _lib.cpattn_poll_error.restype = ctypes.c_int
 _lib.cpattn_status_string.argtypes = [ctypes.c_int]
@@ -835,6 +849,81 @@ def paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, max_seql
     """
     return _binding().paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, max_seqlen,
                                  max_kv_len, softmax_scale, causal, out, lse, workspace, stream)
+
+
+# -------------------------------------------------------- paged cache in 4 bits --
+
+def alloc_fp4_cache(num_pages, page_size, num_kv_heads, head_dim, device=None):
+    """An empty 4-bit cache of keys or of values, uint8 ``[num_pages, num_kv_heads,
+    page_size, 9 * head_dim / 16]`` (torch-owned).  Its last two dimensions are a page
+    of one head, laid out as ``include/cpattn.h`` says, not rows of tokens."""
+    if head_dim not in (64, 128):
+        raise CpattnError(ERR_UNSUPPORTED, "alloc_fp4_cache")
+    return torch.zeros((num_pages, num_kv_heads, page_size, 9 * head_dim // 16),
+                       dtype=torch.uint8, device=device or "cuda")
+
+
+@_traced("cpattn_paged_append_fp4")
+def paged_append_fp4(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, k_scale=1.0,
+                     v_scale=1.0, status=None, stream=None):
+    """New keys and values, quantised to 4 bits, into a paged cache
+    (``cpattn_paged_append_fp4``).
+
+    ``k, v [T, Hk, D]``: bf16, the keys normed and rotated already
+    (:func:`qk_norm_rope`); ``k_cache, v_cache``: see :func:`alloc_fp4_cache`; the
+    others as :func:`paged_append`'s.  ``k_scale``, ``v_scale``: powers of two, the
+    same in every call on the cache.
+    """
+    return _binding().paged_append_fp4(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens,
+                                       k_scale, v_scale, status, stream)
+
+
+@_traced("cpattn_paged_gather_fp4")
+def paged_gather_fp4(k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, total_tokens,
+                     k_scale=1.0, v_scale=1.0, k_out=None, v_out=None, status=None, stream=None):
+    """Cached tokens as packed bf16 keys and values (``cpattn_paged_gather_fp4``):
+    the last ``cu_seqlens[b + 1] - cu_seqlens[b]`` of each sequence's
+    ``kv_lens[b]``; returns ``(k_out, v_out)``, ``[total_tokens, Hk, D]``.
+
+    The rows are exactly what the cache holds; rows behind the last sequence and of
+    tokens without a place are left as they were (``status`` then says so).
+    """
+    return _binding().paged_gather_fp4(k_cache, v_cache, page_table, cu_seqlens, kv_lens,
+                                       total_tokens, k_scale, v_scale, k_out, v_out, status,
+                                       stream)
+
+
+def paged_fp4_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
+                             max_kv_len):
+    n = _lib.cpattn_paged_attn_fp4_workspace_size(total_q, num_seqs, num_heads, num_kv_heads,
+                                                  head_dim, max_seqlen, max_kv_len)
+    if n == 0:
+        raise CpattnError(ERR_INVALID_ARG, "cpattn_paged_attn_fp4_workspace_size")
+    return n
+
+
+def alloc_paged_fp4_workspace(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
+                              max_kv_len, device=None):
+    """A device workspace sized for :func:`paged_attn_fp4` (torch-owned), for this batch
+    and smaller ones of the same heads."""
+    n = paged_fp4_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
+                                 max_kv_len)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+@_traced("cpattn_paged_attn_fp4")
+def paged_attn_fp4(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, max_seqlen, max_kv_len,
+                   k_scale=1.0, v_scale=1.0, softmax_scale=None, causal=True, out=None, lse=None,
+                   workspace=None, stream=None):
+    """:func:`paged_attn` over a 4-bit cache (``cpattn_paged_attn_fp4``); returns
+    ``(out, lse)``.
+
+    ``k_cache, v_cache``: see :func:`alloc_fp4_cache`; ``k_scale``, ``v_scale``: as
+    given to :func:`paged_append_fp4`; the others as :func:`paged_attn`'s.
+    """
+    return _binding().paged_attn_fp4(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens,
+                                     max_seqlen, max_kv_len, k_scale, v_scale, softmax_scale,
+                                     causal, out, lse, workspace, stream)
 
 
 def poll_error(workspace, stream=None):

@@ -1,5 +1,5 @@
 // CPython module `_binding`: argument marshalling of the calls that run once
-// per layer of a decoding step (norm + rotation, paged append, paged attention),
+// per layer of a decoding step (norm + rotation, the paged caches' calls),
 // where the host's time counts.  It does for them what the ctypes binding in
 // cpattn.py does for the others -- checks each tensor's type, device, shape and
 // layout, allocates what was not given, and hands the addresses and PyTorch's
@@ -356,38 +356,36 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
 struct Cache {
   void *k = nullptr, *v = nullptr;
   int64_t pages = 0, page_stride = 0;
-  int size = 0, heads = 0, seqs = 0, row = 0;
+  int size = 0, heads = 0, seqs = 0, row = 0, dim = 0;
   const int32_t *table = nullptr, *cu = nullptr, *kv = nullptr;
 };
 
-// k_cache, v_cache, page_table, cu_seqlens, kv_lens; heads < 0: the cache's.
-Cache cache_args(PyObject* const* a, c10::Device dev, int64_t heads, int64_t D) {
-  Cache c;
-  const at::Tensor& k = tensor(a[0], "k_cache", at::kBFloat16);
-  if (k.dim() != 4)
-    raise(PyExc_ValueError, "k_cache must be [num_pages, page_size, heads, D]");
-  if (heads < 0) heads = k.size(2);
-  c.pages = k.size(0);
-  c.size = as_int(k.size(1), "page_size");
-  c.heads = as_int(heads, "heads");
-  const char* names[2] = {"k_cache", "v_cache"};
-  int64_t strides[2];
-  for (int i = 0; i < 2; ++i) {
-    const at::Tensor& t = tensor(a[i], names[i], at::kBFloat16);
-    on_device(t, names[i], dev);
-    of_shape(t, names[i], {c.pages, c.size, heads, D});
-    strides[i] = c.size * heads * D;
-    if (!t.is_contiguous()) {
-      int64_t want = 1;
-      for (int d = 3; d > 0; --d) {
-        if (t.size(d) > 1 && t.stride(d) != want)
-          raise(PyExc_ValueError, std::string(names[i]) + ": a page must be contiguous");
-        want *= t.size(d);
-      }
-      if (c.pages > 1) strides[i] = t.stride(0);
+// One cache of that shape, its pages contiguous; its address, and the elements from
+// page to page.
+void* page_args(PyObject* o, const char* name, c10::ScalarType dtype, c10::Device dev,
+                c10::IntArrayRef shape, int64_t* stride) {
+  const at::Tensor& t = tensor(o, name, dtype);
+  on_device(t, name, dev);
+  of_shape(t, name, shape);
+  *stride = shape[1] * shape[2] * shape[3];
+  if (!t.is_contiguous()) {
+    int64_t want = 1;
+    for (int d = 3; d > 0; --d) {
+      if (t.size(d) > 1 && t.stride(d) != want)
+        raise(PyExc_ValueError, std::string(name) + ": a page must be contiguous");
+      want *= t.size(d);
     }
-    (i ? c.v : c.k) = t.data_ptr();
+    if (shape[0] > 1) *stride = t.stride(0);
   }
+  return t.data_ptr();
+}
+
+// k_cache and v_cache (a[0], a[1]) of that shape, page_table, cu_seqlens, kv_lens.
+void cache_tensors(Cache& c, PyObject* const* a, c10::ScalarType dtype, c10::Device dev,
+                   c10::IntArrayRef shape) {
+  int64_t strides[2];
+  c.k = page_args(a[0], "k_cache", dtype, dev, shape, strides);
+  c.v = page_args(a[1], "v_cache", dtype, dev, shape, strides + 1);
   if (strides[0] != strides[1])
     raise(PyExc_ValueError, "k_cache and v_cache must have the same page stride");
   c.page_stride = strides[0];
@@ -401,6 +399,35 @@ Cache cache_args(PyObject* const* a, c10::Device dev, int64_t heads, int64_t D) 
       flat(a[2], "page_table", at::kInt, dev, {kv.size(0), table.size(1)}));
   c.cu = static_cast<int32_t*>(flat(a[3], "cu_seqlens", at::kInt, dev, {kv.size(0) + 1}));
   c.kv = static_cast<int32_t*>(flat(a[4], "kv_lens", at::kInt, dev, {kv.size(0)}));
+}
+
+// k_cache, v_cache, page_table, cu_seqlens, kv_lens; heads < 0: the cache's.
+Cache cache_args(PyObject* const* a, c10::Device dev, int64_t heads, int64_t D) {
+  Cache c;
+  const at::Tensor& k = tensor(a[0], "k_cache", at::kBFloat16);
+  if (k.dim() != 4)
+    raise(PyExc_ValueError, "k_cache must be [num_pages, page_size, heads, D]");
+  if (heads < 0) heads = k.size(2);
+  c.pages = k.size(0);
+  c.size = as_int(k.size(1), "page_size");
+  c.heads = as_int(heads, "heads");
+  cache_tensors(c, a, at::kBFloat16, dev, {c.pages, c.size, heads, D});
+  return c;
+}
+
+// The same with 4-bit caches (strides in bytes); D < 0: the cache's.
+Cache fp4_args(PyObject* const* a, c10::Device dev, int64_t heads, int64_t D) {
+  Cache c;
+  const at::Tensor& k = tensor(a[0], "k_cache", at::kByte);
+  if (k.dim() != 4)
+    raise(PyExc_ValueError, "k_cache must be [num_pages, heads, page_size, 9 * D / 16]");
+  if (heads < 0) heads = k.size(1);
+  if (D < 0) D = k.size(3) / 9 * 16;
+  c.pages = k.size(0);
+  c.size = as_int(k.size(2), "page_size");
+  c.heads = as_int(heads, "heads");
+  c.dim = as_int(D, "head_dim");
+  cache_tensors(c, a, at::kByte, dev, {c.pages, heads, c.size, D / 16 * 9});
   return c;
 }
 
@@ -469,6 +496,84 @@ PyObject* paged_attn(PyObject* const* a) {
   return tuple({out.object(), lse.object()});
 }
 
+// k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, k_scale, v_scale, status,
+// stream -> None
+PyObject* paged_append_fp4(PyObject* const* a) {
+  const at::Tensor& k = leading(a[0], "k");
+  const c10::Device dev = k.device();
+  const int64_t T = k.size(0), Hk = k.size(1), D = k.size(2);
+  const Rows kr = rows(a[0], "k", dev, T, Hk, D), vr = rows(a[1], "v", dev, T, Hk, D);
+  const Cache c = fp4_args(a + 2, dev, Hk, D);
+  const float ks = static_cast<float>(real(a[7])), vs = static_cast<float>(real(a[8]));
+  int32_t* status = nullptr;
+  if (a[9] != Py_None) status = static_cast<int32_t*>(flat(a[9], "status", at::kInt, dev, {1}));
+  Call call(dev, a[10]);
+  Call::check(cpattn_paged_append_fp4(kr.at, kr.stride, vr.at, vr.stride, c.k, c.v, c.pages, c.size,
+                                      c.page_stride, c.table, c.row, c.cu, c.kv, c.seqs, T,
+                                      c.heads, c.dim, ks, vs, status, call.stream()),
+              "cpattn_paged_append_fp4");
+  return keep(Py_None);
+}
+
+// k_cache, v_cache, page_table, cu_seqlens, kv_lens, total_tokens, k_scale, v_scale,
+// k_out, v_out, status, stream -> (k_out, v_out)
+PyObject* paged_gather_fp4(PyObject* const* a) {
+  const at::Tensor& cache = tensor(a[0], "k_cache", at::kByte);
+  if (!cache.is_cuda())
+    raise(PyExc_ValueError, "k_cache must be on a CUDA device, got " + cache.device().str());
+  const c10::Device dev = cache.device();
+  const Cache c = fp4_args(a, dev, -1, -1);
+  const int64_t T = number(a[5], "total_tokens");
+  if (T < 0) raise(PyExc_ValueError, "total_tokens must not be negative");
+  const float ks = static_cast<float>(real(a[6])), vs = static_cast<float>(real(a[7]));
+  int32_t* status = nullptr;
+  if (a[10] != Py_None) status = static_cast<int32_t*>(flat(a[10], "status", at::kInt, dev, {1}));
+  Call call(dev, a[11]);
+  const Output ko = rows_out(call, a[8], "k_out", dev, T, c.heads, c.dim);
+  const Output vo = rows_out(call, a[9], "v_out", dev, T, c.heads, c.dim);
+  Call::check(cpattn_paged_gather_fp4(c.k, c.v, c.pages, c.size, c.page_stride, c.table, c.row,
+                                      c.cu, c.kv, c.seqs, T, c.heads, c.dim, ks, vs, ko.r.at,
+                                      ko.r.stride, vo.r.at, vo.r.stride, status, call.stream()),
+              "cpattn_paged_gather_fp4");
+  return tuple({ko.object(), vo.object()});
+}
+
+// q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, max_seqlen, max_kv_len, k_scale,
+// v_scale, softmax_scale, causal, out, lse, workspace, stream -> (out, lse)
+PyObject* paged_attn_fp4(PyObject* const* a) {
+  const at::Tensor& q = leading(a[0], "q");
+  const c10::Device dev = q.device();
+  const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+  if (!q.is_contiguous()) raise(PyExc_ValueError, "q must be contiguous");
+  const Cache c = fp4_args(a + 1, dev, -1, D);
+  const int max_q = as_int(number(a[6], "max_seqlen"), "max_seqlen");
+  const int max_kv = as_int(number(a[7], "max_kv_len"), "max_kv_len");
+  const float ks = static_cast<float>(real(a[8])), vs = static_cast<float>(real(a[9]));
+  const float scale =
+      a[10] == Py_None ? 1.f / std::sqrt(static_cast<float>(D)) : static_cast<float>(real(a[10]));
+  const bool causal = truth(a[11]);
+  Call call(dev, a[15]);
+  const Output out = flat_out(call, a[12], "out", at::kBFloat16, dev, {T, H, D});
+  const Output lse = flat_out(call, a[13], "lse", at::kFloat, dev, {T, H});
+  int64_t bytes;
+  if (a[14] != Py_None) {
+    bytes = tensor(a[14], "workspace", at::kByte).numel();
+  } else {
+    bytes = static_cast<int64_t>(cpattn_paged_attn_fp4_workspace_size(
+        T, c.seqs, as_int(H, "heads"), c.heads, c.dim, max_q, max_kv));
+    // Sizes the call itself will refuse, with its status.
+    if (bytes == 0) bytes = 256;
+  }
+  const Output ws = flat_out(call, a[14], "workspace", at::kByte, dev, {bytes});
+  Call::check(cpattn_paged_attn_fp4(q.data_ptr(), c.k, c.v, c.pages, c.size, c.page_stride, c.table,
+                                    c.row, c.cu, c.kv, c.seqs, T, max_q, max_kv,
+                                    as_int(H, "heads"), c.heads, c.dim, ks, vs, scale, causal,
+                                    out.r.at, static_cast<float*>(lse.r.at), ws.r.at,
+                                    static_cast<size_t>(bytes), call.stream()),
+              "cpattn_paged_attn_fp4");
+  return tuple({out.object(), lse.object()});
+}
+
 // Every call: its number of arguments, and no C++ exception past this point.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -502,6 +607,9 @@ PyMethodDef g_methods[] = {
     method<qk_norm_rope_bwd, 17>("qk_norm_rope_bwd"),
     method<paged_append, 16>("paged_append"),
     method<paged_attn, 14>("paged_attn"),
+    method<paged_append_fp4, 11>("paged_append_fp4"),
+    method<paged_gather_fp4, 12>("paged_gather_fp4"),
+    method<paged_attn_fp4, 16>("paged_attn_fp4"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -337,4 +337,47 @@ cudaError_t launch_paged_tile(const CUtensorMap& tq, const CUtensorMap& tk, cons
                               cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedParams& p, int D, int num_sms, cudaStream_t stream);
 
+// The 4-bit cache (fp4.cuh, paged_fp4*.cu): bytes [pages, KV heads, page size * 9 D / 16],
+// a page contiguous, page_stride bytes from page to page.
+struct Fp4CacheParams {
+  const __nv_bfloat16 *k, *v;        // append: inputs, [T, KV heads, D]
+  __nv_bfloat16 *k_out, *v_out;      // gather: outputs, likewise
+  uint8_t *k_cache, *v_cache;
+  long long k_stride, v_stride;      // elements from token to token
+  const int *cu_seqlens, *kv_lens, *page_table;
+  int num_seqs, num_pages, page_shift, max_pages, kv_heads;
+  long long page_stride, total_tokens;
+  float k_scale, v_scale;            // gather: the caches' powers of two; append: 1 / them
+  int* status;
+};
+
+cudaError_t launch_fp4_append(const Fp4CacheParams& p, int D, cudaStream_t stream);
+cudaError_t launch_fp4_gather(const Fp4CacheParams& p, int D, cudaStream_t stream);
+
+constexpr int kFp4OutPage = 128;  // tokens of a bf16 page that the tile kernel reads
+
+struct Fp4PagesParams {
+  const uint8_t *k_cache, *v_cache;
+  __nv_bfloat16 *k_out, *v_out;      // [num_seqs * out_pages, 128, KV heads, D]
+  int* out_table;                    // [num_seqs, out_pages]
+  const int *kv_lens, *page_table;
+  int num_seqs, num_pages, page_shift, max_pages, kv_heads, out_pages, max_kv_len;
+  long long page_stride;
+  float v_scale;
+  WsHeader* hdr;
+};
+
+// Follows the schedule kernel (as its programmatic dependent).
+cudaError_t launch_fp4_pages(const Fp4PagesParams& p, int D, cudaStream_t stream);
+
+// Few rows: PagedParams with the caches' addresses and strides in bytes.
+struct Fp4RowsParams {
+  PagedParams p;
+  const uint8_t *k_cache, *v_cache;
+  long long page_stride;
+  float v_scale;                     // (p.scale_log2 has the keys')
+};
+
+cudaError_t launch_fp4_rows(const Fp4RowsParams& p, int D, cudaStream_t stream);
+
 }  // namespace cpattn

@@ -1,0 +1,681 @@
+// Attention of few rows over a paged KV cache in 4 bits (fp4.cuh): one token a
+// sequence, or a few, for every query head that shares a KV head.
+//
+// The work is cut as for the bf16 cache (paged_rows.cu): a CTA of 4 warps has one
+// block of 8, 16 or 32 rows of one KV head and one split of the keys, and each warp
+// takes every fourth step of the split on its own, with its own ring of stages, its
+// own softmax state and no barrier until the states are joined.  What differs is what
+// bounds it: a key and its value are 9 D / 8 bytes instead of 4 D, so at the copy
+// bandwidth an SM has 98 cycles for a tile of 16 keys of 128 features and their
+// values, in which 4,096 codes become fp16 operands.  (Measured rates of an SM: 43
+// conversions of two codes a cycle with the byte taken out of its word, 64 packed
+// multiplications, 64 permutations, 0.57 matrix instructions.)  So:
+// * keys and values are the left operand of 16 x 8 x 16 matrix instructions, whose
+//   16 rows they fill, and the queries are the right one: 8 rows cost 8 instructions
+//   for a tile's scores, not 16;
+// * scores come out as [keys, rows]; the matrix transpose that P needs between the
+//   products is one instruction for 8 x 8;
+// * a code pair (features 2 i and 2 i + 1 of one key) is a pair of fp16 as it comes
+//   out of the conversion.  Keys take it as it is.  The values' operand has pairs of
+//   keys: with one block of 8 rows, the pair is used as two columns of the operand
+//   instead, and P's column for the other feature is zero, so each feature of a pair
+//   costs a product (8 more instructions a tile instead of 32 permutations a lane);
+//   with more rows the pairs are permuted;
+// * codes times scales are exact in fp16, the queries (each row times a power of two,
+//   which the score's factor takes back) too; P is rounded to fp16 (2^-12);
+// * K and V come by bulk copies, one a page and operand, a few lanes issuing them.
+//
+// Softmax: p = 2^(s scale log2 e - m + 11), a running reference m per row that moves
+// when a score exceeds it by 4 powers of two; p is then below 2^15 and keeps fp16's
+// 11 bits down to 2^-25 of the largest weight.  l sums p in fp32.
+#include <cuda_bf16.h>
+
+#include "fp4.cuh"
+#include "kernels.h"
+#include "paged_plan.cuh"
+#include "ptx.cuh"
+
+namespace cpattn {
+
+namespace {
+
+constexpr int kF4Warps = 4;
+constexpr int kF4RowsThreads = kF4Warps * 32;
+constexpr float kNegInfF = -__builtin_huge_valf();
+constexpr float kLn2F = 0.69314718055994530942f;
+constexpr float kLog2eF = 1.44269504088896340736f;
+constexpr float kMoveByF = 4.f;  // powers of two
+constexpr float kLiftF = 11.f;   // powers of two of the largest weight
+
+enum : int { kErrArgF4 = 1, kErrTimeoutF4 = 6 };
+
+template <int D, int NT>
+struct Fp4RowsCfg {
+  static constexpr int kTiles = D == 128 ? 2 : 4;  // tiles of a step
+  static constexpr int kKeys = kTiles * kFp4Tile;
+  static constexpr int kHalf = kTiles * Fp4<D>::kTileBytes;  // K (or V) of a step
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = 3;
+  static constexpr int kRing = kF4Warps * kStages * kStage;  // 55 KB
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kJoin = kF4Warps * kRows * D * 4;
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+  // Tiles whose scores are taken together.
+  static constexpr int kPass = NT == 4 ? (D == 128 ? 1 : 2) : 2;
+  static constexpr int kCtas = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // of an SM
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128_zero(uint32_t a) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+}
+
+}  // namespace
+
+template <int D, int NT, bool PLAN>
+__global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
+    fp4_rows_kernel(const Fp4RowsParams fp) {
+  using C = Fp4RowsCfg<D, NT>;
+  using F = Fp4<D>;
+  const PagedParams& p = fp.p;
+  constexpr int kRows = C::kRows;
+  constexpr bool kPairs = NT > 1;   // permuted pairs of keys
+  constexpr int kM = D / 16;        // products of a tile's scores
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kF4Warps][kRows], s_l[kF4Warps][kRows];
+  __shared__ __align__(8) uint64_t s_full[kF4Warps][C::kStages];
+  __shared__ int s_last, s_abort;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int Hk = p.num_kv_heads, G = p.group;
+  const int e = static_cast<int>(blockIdx.x) / Hk;
+  const int h = static_cast<int>(blockIdx.x) - e * Hk;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  PagedWork w;
+  if (PLAN) {
+    const PagedPlan plan = make_plan(p, lane);
+    if (e >= plan.splits) return;
+    w = plan_split(p, plan, e);
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n_work = __ldcg(&p.hdr->n_items);
+    const int err0 = __ldcg(&p.hdr->error);
+    const int4* wp = reinterpret_cast<const int4*>(p.work + e);
+    const int4 w0 = __ldcg(wp), w1 = __ldcg(wp + 1), w2 = __ldcg(wp + 2);
+    if (e >= n_work) return;
+    if (__syncthreads_or(says_timeout(err0))) return;
+    w.tok0 = w0.x;
+    w.q_len = w0.y;
+    w.kv_len = w0.z;
+    w.seq = w0.w;
+    w.blk = w1.x;
+    w.kv_lo = w1.y;
+    w.kv_hi = w1.z;
+    w.slot = w1.w;
+    w.slot0 = w2.x;
+    w.n = w2.y;
+    w.item = w2.z;
+  }
+  const int tok0 = w.tok0, q_len = w.q_len, kv_len = w.kv_len, seq = w.seq;
+  const int blk = w.blk, kv_lo = w.kv_lo, kv_hi = w.kv_hi, slot = w.slot;
+  // Rows of this block: [row0, row0 + kRows), those below 0 are not there.
+  const int all_rows = q_len * G;
+  const int n_blk = (all_rows + kRows - 1) / kRows;
+  const int row0 = all_rows - (n_blk - blk) * kRows;
+
+  // Steps of this warp: keys [kv_lo + (warp + 4 i) kKeys, + kKeys).
+  const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;
+  const int page_tiles = 1 << (p.page_shift - 4);
+  const int all_steps = (kv_hi - kv_lo + C::kKeys - 1) / C::kKeys;
+  const int steps = all_steps > warp ? (all_steps - warp + kF4Warps - 1) / kF4Warps : 0;
+  auto step_key = [&](int i) { return kv_lo + (warp + i * kF4Warps) * C::kKeys; };
+  auto step_tiles = [&](int i) {
+    return min(C::kTiles, (kv_hi - step_key(i) + kFp4Tile - 1) / kFp4Tile);
+  };
+  const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
+  uint64_t* full = s_full[warp];
+  // A step's tiles come in runs that share a page; lane 2 r copies run r of K, lane
+  // 2 r + 1 of V.  Its page number is read a step ahead.
+  const int run_tiles = min(C::kTiles, page_tiles);
+  const int run_at = (lane >> 1) * run_tiles;
+  const uint8_t* cache = (lane & 1) ? fp.v_cache : fp.k_cache;
+  const size_t head_at = static_cast<size_t>(h) * page_tiles * F::kTileBytes;
+  auto page_of = [&](int i) {
+    return i < steps && run_at < step_tiles(i)
+               ? __ldg(pages + ((step_key(i) + run_at * kFp4Tile) >> p.page_shift))
+               : 0;
+  };
+  int next_page = page_of(0);
+  bool bad_page = false;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
+    fence_mbarrier_init();
+  }
+  if (threadIdx.x == 0) s_abort = 0;
+  __syncthreads();
+  auto copy = [&](int i) {
+    if (i >= steps) return;
+    const int page = next_page;
+    next_page = page_of(i + 1);
+    const int st = i % C::kStages;
+    const int n = min(run_tiles, step_tiles(i) - run_at);  // tiles of this lane's run
+    const bool have = n > 0 && lane < 2 * C::kTiles;
+    const bool good = have && page >= 0 && page < p.num_pages;
+    const uint32_t bytes = good ? n * F::kTileBytes : 0;
+    const uint32_t dst = ring + st * C::kStage + (lane & 1) * C::kHalf + run_at * F::kTileBytes;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(full + st, all);
+    __syncwarp();
+#ifdef CPATTN_FAULT_INJECT_DROP_P
+    if (blockIdx.x == 0 && warp == 0 && i == 0) return;
+#endif
+    if (good) {
+      const int at = ((step_key(i) + run_at * kFp4Tile) >> 4) & (page_tiles - 1);
+      bulk_load(dst, cache + static_cast<size_t>(page) * fp.page_stride + head_at +
+                         static_cast<size_t>(at) * F::kTileBytes,
+                bytes, full + st);
+    } else if (have) {
+      // Its keys or values count as zeros: their scales are.
+      bad_page = true;
+      for (int x = 0; x < n; ++x)
+        for (int y = 0; y < D; y += 16) sts128_zero(dst + x * F::kTileBytes + F::kScales + y);
+      fence_proxy_async_smem();
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) copy(i);
+
+  // The queries as right operands: lane (g, t) has row g of each block of eight,
+  // features [t D / 4, + D / 4), as fp16 times a power of two that brings the row's
+  // largest below 2^15.
+  uint32_t q[NT][kM][2];
+  float sc[NT][2];  // from a score to the exponent, rows 2 t and 2 t + 1
+  int lim[NT][2];   // keys below it are visible
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = row0 + nt * 8 + g;
+    const bool in = row >= 0;
+    const int tok = in ? row / G : 0;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + (static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (in ? row - tok * G : 0)) * D +
+        t * (D / 4));
+    uint32_t x[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      x[4 * i] = v.x;
+      x[4 * i + 1] = v.y;
+      x[4 * i + 2] = v.z;
+      x[4 * i + 3] = v.w;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^(14 - exponent of the largest); its inverse is a normal number too.
+    const int up = min(252, 268 - static_cast<int>(top >> 7));
+    const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        q[nt][m][i] = pack_f16x2(__uint_as_float(x[2 * m + i] << 16) * f,
+                                 __uint_as_float(x[2 * m + i] & 0xffff0000u) * f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // A normal number: masked scores (-inf) and zeros are multiplied by it.
+      sc[nt][i] = fminf(fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + i) * 4) * p.scale_log2,
+                              1.17549435e-38f), 3.40282347e38f);
+      const int r = row0 + nt * 8 + 2 * t + i;
+      lim[nt][i] = r < 0 ? 0 : (p.causal ? kv_len - q_len + r / G + 1 : kv_len);
+    }
+  }
+  // Steps ending at or below this key need no mask (rows are in order, so the
+  // block's first row sees the fewest keys).
+  const int first_tok = max(row0, 0) / G;
+  const int free_end = row0 < 0 ? 0 : (p.causal ? kv_len - q_len + first_tok + 1 : kv_len);
+
+  // Lane (g, t) accumulates rows 2 t and 2 t + 1 of features g D / 8 + 2 i and + 1, i
+  // below D / 16: [i][feature][row] with permuted pairs, else [i / 2][feature][i % 2][row].
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = kNegInfF;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[nt][i][x] = 0.f;
+  }
+
+  bool failed = false;
+  int step = 0;
+#pragma unroll 1
+  for (; step < steps; ++step) {
+    const int st = step % C::kStages;
+    const bool landed = wait_bounded(full + st, (step / C::kStages) & 1, &s_abort);
+    if (__any_sync(0xffffffffu, !landed)) {
+      failed = true;
+      break;
+    }
+    copy(step + C::kStages - 1);
+    const int key0 = step_key(step);
+    const int tiles = step_tiles(step);
+    const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
+#pragma unroll
+    for (int pass = 0; pass < C::kTiles; pass += C::kPass) {
+      if (pass > 0 && pass >= tiles) break;
+      float s[C::kPass][NT][4];
+#pragma unroll
+      for (int u = 0; u < C::kPass; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[u][nt][x] = 0.f;
+        if (u > 0 && pass + u >= tiles) continue;
+        // Rows of the left operand: token 2 g, and 2 g + 1 as row g + 8.
+        const uint32_t tile = kb + (pass + u) * F::kTileBytes;
+#pragma unroll
+        for (int gg = 0; gg < D / 64; ++gg) {
+          const int j = t * (D / 64) + gg;
+          const uint4 k4 = lds128(tile + F::place(j, g));
+          const uint32_t both = e4m3x2_to_f16(lds16(tile + F::kScales + j * kFp4Tile + 2 * g));
+          const uint32_t s0 = __byte_perm(both, 0, 0x1010), s1 = __byte_perm(both, 0, 0x3232);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t a[4], b[4];
+            fp4x8_to_f16(half ? k4.y : k4.x, a);
+            fp4x8_to_f16(half ? k4.w : k4.z, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = mul_f16x2(a[i], s0);
+              b[i] = mul_f16x2(b[i], s1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t op[4] = {a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1]};
+              const int mm = gg * 4 + half * 2 + i;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816_f16(s[u][nt], op, q[nt][mm][0], q[nt][mm][1]);
+            }
+          }
+        }
+      }
+      if (key0 + (pass + C::kPass) * kFp4Tile > free_end || pass + C::kPass > tiles) {
+#pragma unroll
+        for (int u = 0; u < C::kPass; ++u)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = key0 + (pass + u) * kFp4Tile + 2 * g + (x >> 1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              if (key >= lim[nt][x & 1] || key >= kv_hi) s[u][nt][x] = kNegInfF;
+          }
+      }
+      bool move = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = kNegInfF;
+#pragma unroll
+          for (int u = 0; u < C::kPass; ++u) v = fmax3(v, s[u][nt][i], s[u][nt][i + 2]);
+          top[nt][i] = v * sc[nt][i];
+          move = move || top[nt][i] > m[nt][i] + kMoveByF;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v = top[nt][i];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float mn = fmaxf(m[nt][i], v);
+            const float alpha = m[nt][i] == kNegInfF ? 0.f : ex2_approx(m[nt][i] - mn);
+            m[nt][i] = mn;
+            l[nt][i] *= alpha;
+#pragma unroll
+            for (int f = 0; f < D / 16; ++f) {
+              o[nt][f][i] *= alpha;
+              o[nt][f][i + 2] *= alpha;
+            }
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < C::kPass; ++u) {
+        if (u > 0 && pass + u >= tiles) continue;
+        // P of this lane's row g: pa tokens 4 t and 4 t + 2, pb 4 t + 1 and 4 t + 3.
+        uint32_t pa[NT], pb[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float e2[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float mr = m[nt][x & 1];
+            const float off = mr == kNegInfF ? kLiftF : kLiftF - mr;
+            e2[x] = ex2_approx(fmaf(s[u][nt][x], sc[nt][x & 1], off));
+          }
+          l[nt][0] += e2[0] + e2[2];
+          l[nt][1] += e2[1] + e2[3];
+          pa[nt] = transpose_8x8(pack_f16x2(e2[0], e2[1]));
+          pb[nt] = transpose_8x8(pack_f16x2(e2[2], e2[3]));
+        }
+        const uint32_t tile = vb + (pass + u) * F::kTileBytes;
+        const int j = D == 128 ? g : g >> 1;
+        const uint4 v01 = lds128(tile + F::place(j, 2 * t));
+        const uint4 v23 = lds128(tile + F::place(j, 2 * t + 1));
+        uint32_t sb = lds32(tile + F::kScales + j * kFp4Tile + 4 * t);
+        // What lies behind the cache's end has weight 0, and a NaN there is one.
+        const int left = kv_len - (key0 + (pass + u) * kFp4Tile);
+        if (left < kFp4Tile) {
+          const int n = left - 4 * t;
+          sb = n <= 0 ? 0u : (n >= 4 ? sb : sb & ((1u << (8 * n)) - 1u));
+        }
+        const uint32_t s01 = e4m3x2_to_f16(sb), s23 = e4m3x2_to_f16(sb >> 16);
+        // Words of the four tokens, eight features each.
+        constexpr int kW = D / 64;
+        uint32_t wd[4][kW];
+        if (D == 128) {
+          wd[0][0] = v01.x;
+          wd[0][kW - 1] = v01.y;
+          wd[1][0] = v01.z;
+          wd[1][kW - 1] = v01.w;
+          wd[2][0] = v23.x;
+          wd[2][kW - 1] = v23.y;
+          wd[3][0] = v23.z;
+          wd[3][kW - 1] = v23.w;
+        } else {
+          const bool hi = g & 1;
+          wd[0][0] = hi ? v01.y : v01.x;
+          wd[1][0] = hi ? v01.w : v01.z;
+          wd[2][0] = hi ? v23.y : v23.x;
+          wd[3][0] = hi ? v23.w : v23.z;
+        }
+        if (kPairs) {
+          const uint32_t s02 = __byte_perm(s01, s23, 0x5410), s13 = __byte_perm(s01, s23, 0x7632);
+#pragma unroll
+          for (int k = 0; k < kW; ++k) {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fp4x8_to_f16(wd[i][k], x[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t op[4] = {
+                  mul_f16x2(__byte_perm(x[0][i], x[2][i], 0x5410), s02),
+                  mul_f16x2(__byte_perm(x[0][i], x[2][i], 0x7632), s02),
+                  mul_f16x2(__byte_perm(x[1][i], x[3][i], 0x5410), s13),
+                  mul_f16x2(__byte_perm(x[1][i], x[3][i], 0x7632), s13)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816_f16(o[nt][k * 4 + i], op, pa[nt], pb[nt]);
+            }
+          }
+        } else {
+          const uint32_t sx[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                                  __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+          // P with the other feature's column zero, tokens (0, 2) and (1, 3).
+          const uint32_t lo[2][2] = {{pa[0] & 0xffffu, pa[0] >> 16}, {pb[0] & 0xffffu, pb[0] >> 16}};
+          const uint32_t hi[2][2] = {{pa[0] << 16, pa[0] & 0xffff0000u},
+                                     {pb[0] << 16, pb[0] & 0xffff0000u}};
+#pragma unroll
+          for (int k = 0; k < kW; ++k) {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              fp4x8_to_f16(wd[i][k], x[i]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) x[i][y] = mul_f16x2(x[i][y], sx[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t op[4] = {x[z][i], x[z][i + 1], x[z + 2][i], x[z + 2][i + 1]};
+                mma_16816_f16(o[0][k * 4 + i], op, lo[z][0], lo[z][1]);
+                mma_16816_f16(o[0][k * 4 + i + 1], op, hi[z][0], hi[z][1]);
+              }
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage may be filled again
+  }
+  if (failed) {
+    s_abort = 1;
+    // Copies in flight still write to this CTA's memory.
+    for (int i = step; i < min(steps, step + C::kStages - 1); ++i) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(full + i % C::kStages, (i / C::kStages) & 1) &&
+             global_timer_ns() - t0 < 200000000ull) {
+      }
+    }
+  }
+
+  // Join the warps' states (their rings are done with) and write the rows.
+  const int fault = __syncthreads_or((bad_page ? kErrArgF4 : 0)) ? kErrArgF4 : 0;
+  const bool gone = __syncthreads_or(failed);
+  if (threadIdx.x == 0) {
+    const int error = gone ? kErrTimeoutF4 : fault;
+    if (PLAN) p.cta_error[blockIdx.x] = error;
+    else if (error) atomicCAS(&p.hdr->error, 0, error);
+  }
+  float* so = reinterpret_cast<float*>(smem) + warp * kRows * D;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = nt * 8 + 2 * t + i;
+      float sum = l[nt][i];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (g == 0) {
+        s_m[warp][r] = m[nt][i] - kLiftF;
+        s_l[warp][r] = sum;
+      }
+#pragma unroll
+      for (int f = 0; f < D / 16; ++f)
+        *reinterpret_cast<float2*>(so + r * D + g * (D / 8) + 2 * f) =
+            kPairs ? make_float2(o[nt][f][i], o[nt][f][i + 2])
+                   : make_float2(o[nt][f & ~1][i + 2 * (f & 1)], o[nt][f | 1][i + 2 * (f & 1)]);
+    }
+  __syncthreads();
+  // Joins the warps' states: to the partial results of `to` (a slot), or to
+  // the output (to < 0), times `unit`.
+  auto join = [&](int to, float unit) {
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (int x = threadIdx.x; x < kRows * (D / 4); x += kF4RowsThreads) {
+      const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+      const int row = row0 + r;
+      if (row < 0) continue;
+      float top = kNegInfF;
+#pragma unroll
+      for (int v = 0; v < kF4Warps; ++v) top = fmaxf(top, s_m[v][r]);
+      float den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < kF4Warps; ++v) {
+        // A warp without a visible key has l = 0 and O = 0 (or NaN in both,
+        // which the row then shows).
+        const float f = s_m[v][r] == kNegInfF ? 1.f : ex2_approx(s_m[v][r] - top);
+        den = fmaf(f, s_l[v][r], den);
+        const float4 y = *reinterpret_cast<const float4*>(all + (v * kRows + r) * D + c);
+        acc.x = fmaf(f, y.x, acc.x);
+        acc.y = fmaf(f, y.y, acc.y);
+        acc.z = fmaf(f, y.z, acc.z);
+        acc.w = fmaf(f, y.w, acc.w);
+      }
+      const float inv = den == 0.f ? 0.f : unit / den;
+      const float ref = top == kNegInfF ? 0.f : top;
+      const float lse = den == 0.f ? kNegInfF : (ref + __log2f(den)) * kLn2F;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (to >= 0) {
+        const size_t part = (static_cast<size_t>(to) * Hk + h) * kRows + r;
+        *reinterpret_cast<float4*>(p.o_part + part * D + c) = acc;
+        if (c == 0) p.lse_part[part] = lse;
+      } else {
+        const int tok = row / G;
+        const size_t at_row =
+            static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (row - tok * G);
+        *reinterpret_cast<uint2*>(p.out + at_row * D + c) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (c == 0 && p.lse != nullptr) p.lse[at_row] = lse;
+      }
+    }
+  };
+  join(slot, fp.v_scale);
+  if (slot < 0 || PLAN || NT > 2) return;  // else paged_merge_kernel joins them
+
+  // The last of an item's splits to be done joins them all, in their order:
+  // each warp takes every fourth split, with its own running maximum.
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(p.arrived + static_cast<size_t>(w.item) * Hk + h, 1) == w.n - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
+  const int splits = w.n;
+  const size_t part0 = (static_cast<size_t>(w.slot0) * Hk + h) * kRows;
+  const size_t pitch = static_cast<size_t>(Hk) * kRows;  // rows from split to split
+  constexpr int kPer = D / 32;                          // floats of a row each lane owns
+  constexpr int kAhead = 4;                             // splits in flight of each of
+  constexpr int kAbreast = 4;                           // so many rows
+  for (int r0 = max(0, -row0); r0 < kRows; r0 += kAbreast) {
+    float mx[kAbreast], sum[kAbreast], acc[kAbreast][kPer];
+#pragma unroll
+    for (int i = 0; i < kAbreast; ++i) {
+      mx[i] = kNegInfF;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int z = 0; z < kPer; ++z) acc[i][z] = 0.f;
+    }
+    for (int s0 = warp; s0 < splits; s0 += kAhead * kF4Warps) {
+      float x[kAbreast][kAhead], v[kAbreast][kAhead][kPer];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int s = s0 + u * kF4Warps;
+#pragma unroll
+        for (int i = 0; i < kAbreast; ++i) {
+          x[i][u] = kNegInfF;
+#pragma unroll
+          for (int z = 0; z < kPer; ++z) v[i][u][z] = 0.f;
+          if (s < splits && r0 + i < kRows) {
+            const size_t part = part0 + s * pitch + r0 + i;
+            x[i][u] = __ldcg(p.lse_part + part) * kLog2eF;
+            const float* src = p.o_part + part * D + lane * kPer;
+            if (kPer == 4) {
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+              v[i][u][0] = f.x;
+              v[i][u][1] = f.y;
+              v[i][u][2 % kPer] = f.z;
+              v[i][u][3 % kPer] = f.w;
+            } else {
+              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+              v[i][u][0] = f.x;
+              v[i][u][1] = f.y;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAbreast; ++i) {
+        float mn = mx[i];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) mn = fmaxf(mn, x[i][u]);
+        const float alpha = mx[i] == kNegInfF ? 0.f : ex2_approx(mx[i] - mn);
+        mx[i] = mn;
+        sum[i] *= alpha;
+#pragma unroll
+        for (int z = 0; z < kPer; ++z) acc[i][z] *= alpha;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const float f = x[i][u] == kNegInfF ? 0.f : ex2_approx(x[i][u] - mn);
+          sum[i] += f;
+#pragma unroll
+          for (int z = 0; z < kPer; ++z) acc[i][z] = fmaf(f, v[i][u][z], acc[i][z]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAbreast; ++i) {
+      const int r = r0 + i;
+      if (r >= kRows) break;
+      if (lane == 0) {
+        s_m[warp][r] = mx[i];
+        s_l[warp][r] = sum[i];
+      }
+#pragma unroll
+      for (int z = 0; z < kPer; z += 2)
+        *reinterpret_cast<float2*>(so + r * D + lane * kPer + z) =
+            make_float2(acc[i][z], acc[i][z + 1]);
+    }
+  }
+  __syncthreads();
+  join(-1, 1.f);
+}
+
+template <int D, int NT, bool PLAN>
+static cudaError_t launch_fp4_rows_t(const Fp4RowsParams& p, cudaStream_t stream) {
+  using C = Fp4RowsCfg<D, NT>;
+  auto kern = fp4_rows_kernel<D, NT, PLAN>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.p.max_work * p.p.num_kv_heads));
+  cfg.blockDim = dim3(kF4RowsThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PLAN ? 0 : 1;  // after the schedule kernel
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, int NT>
+static cudaError_t launch_fp4_rows_p(const Fp4RowsParams& p, cudaStream_t stream) {
+  return p.p.shape.plan ? launch_fp4_rows_t<D, NT, true>(p, stream)
+                        : launch_fp4_rows_t<D, NT, false>(p, stream);
+}
+
+template <int D>
+static cudaError_t launch_fp4_rows_d(const Fp4RowsParams& p, cudaStream_t stream) {
+  return p.p.shape.rows == 8    ? launch_fp4_rows_p<D, 1>(p, stream)
+         : p.p.shape.rows == 16 ? launch_fp4_rows_p<D, 2>(p, stream)
+                                : launch_fp4_rows_p<D, 4>(p, stream);
+}
+
+cudaError_t launch_fp4_rows(const Fp4RowsParams& p, int D, cudaStream_t stream) {
+  return D == 64 ? launch_fp4_rows_d<64>(p, stream) : launch_fp4_rows_d<128>(p, stream);
+}
+
+}  // namespace cpattn

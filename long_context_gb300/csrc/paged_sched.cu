@@ -536,7 +536,8 @@ __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(const PagedPara
       error |= __ldcg(p.cta_error + i);
     error = __syncthreads_or(error);
     if (threadIdx.x == 0) {
-      p.hdr->error = plan.bad || error ? 1 : 0;  // CPATTN_ERR_INVALID_ARG
+      // CPATTN_ERR_INVALID_ARG, or a wait's CPATTN_ERR_DEVICE_TIMEOUT.
+      p.hdr->error = plan.bad || (error & 1) ? 1 : error;
       p.hdr->n_items = plan.splits;
       p.hdr->pad[0] = plan.merges;
     }

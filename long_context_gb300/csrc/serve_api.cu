@@ -1,5 +1,5 @@
-// Host side of the C ABI's norm + rotation and paged-cache calls (declared in
-// include/cpattn.h): argument checks, workspace layout and kernel launches.
+// Host side of the C ABI's norm + rotation and paged-cache calls, bf16 and 4-bit
+// (declared in include/cpattn.h): argument checks, workspace layout and kernel launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "cpattn.h"
+#include "fp4.cuh"
 #include "kernels.h"
 #include "paged_plan.cuh"
 
@@ -155,6 +156,119 @@ size_t paged_workspace(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_
   }
   return most;
 }
+
+// The workspace's parts, and the grid's size.
+void set_workspace(PagedParams& p, uint8_t* ws, const PagedLayout& lay) {
+  p.hdr = reinterpret_cast<WsHeader*>(ws);
+  p.first = reinterpret_cast<int*>(ws + lay.first_off);
+  p.work = reinterpret_cast<PagedWork*>(ws + lay.work_off);
+  p.merge = reinterpret_cast<PagedMerge*>(ws + lay.merge_off);
+  p.arrived = reinterpret_cast<int*>(ws + lay.arrived_off);
+  p.cta_error = reinterpret_cast<int*>(ws + lay.error_off);
+  p.o_part = reinterpret_cast<float*>(ws + lay.o_off);
+  p.lse_part = reinterpret_cast<float*>(ws + lay.lse_off);
+  // The grid: no more splits than units, nor (a plan's items are at most num_seqs)
+  // than one round when they are made to fit one.  CTAs without work cost a small
+  // step a round of their own.
+  p.max_work = lay.max_work;
+  const int64_t units = (static_cast<int64_t>(p.max_kv_len) + p.shape.unit - 1) / p.shape.unit;
+  const int64_t items = p.total_q * p.group / p.shape.rows + p.num_seqs;
+  if (units < 1) p.max_work = p.max_work < items ? p.max_work : items;
+  else if (p.max_work / units >= items) p.max_work = items * units;
+  const int64_t lanes = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
+  if (p.shape.plan && 2 * lanes <= p.shape.round && p.max_work > p.shape.round / p.num_kv_heads)
+    p.max_work = p.shape.round / p.num_kv_heads;
+  p.max_slots = lay.max_slots;
+}
+
+// Lists of short items are never cut; after a plan the merge also writes the error word.
+bool merges(const PagedParams& p) {
+  return !p.shape.join && (p.shape.plan || p.max_kv_len > p.shape.keep * p.shape.unit);
+}
+
+// Few rows over the 4-bit cache: blocks of 8, 16 or 32 rows and, above that, several of
+// 32; kFp4RowsMost rows of a KV head and more read the caches into bf16 pages first
+// and go through the tile kernel.
+constexpr int64_t kFp4RowsMost = 128;
+
+PagedShape fp4_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
+  PagedShape s = paged_shape(group, max_seqlen, num_seqs);
+  const int64_t rows = group * max_seqlen;
+  if (rows > kFp4RowsMost) return s;
+  s.tiles = false;
+  s.plan = rows <= 32 && num_seqs <= kPlanSeqs;
+  s.join = rows <= 16 && !s.plan;
+  s.rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  s.unit = 64;
+  s.min_units = 24;
+  s.whole = s.keep = 1;
+  s.ctas = 608;
+  s.round = 152 * (rows <= 8 ? 4 : (rows <= 16 ? 3 : 2));  // CTAs that an SM holds
+  return s;
+}
+
+// The bf16 pages that the tile kernel reads: their table, keys and values.
+struct Fp4Pages {
+  int64_t pages;  // of a sequence
+  size_t k_off, v_off, total;
+};
+
+Fp4Pages fp4_pages(int32_t B, int32_t Hk, int32_t D, int32_t max_kv_len) {
+  Fp4Pages f;
+  f.pages = (static_cast<int64_t>(max_kv_len) + kFp4OutPage - 1) / kFp4OutPage;
+  const size_t all = static_cast<size_t>(f.pages) * B;
+  const size_t bytes = serve_align(all * kFp4OutPage * Hk * D * 2);
+  f.k_off = serve_align(all * sizeof(int));
+  f.v_off = f.k_off + bytes;
+  f.total = f.v_off + bytes;
+  return f;
+}
+
+// Bytes for this batch and every smaller one (see paged_workspace).
+size_t fp4_workspace(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t D,
+                     int32_t max_seqlen, int32_t max_kv_len) {
+  const int64_t group = H / Hk;
+  size_t most = 0;
+  for (const int64_t rows : {int64_t(8), int64_t(16), int64_t(32), kFp4RowsMost,
+                             group * max_seqlen}) {
+    const int32_t len = static_cast<int32_t>(std::min<int64_t>(max_seqlen, rows / group));
+    for (const int32_t seqs : {B, std::min(B, kPlanSeqs)})
+      most = std::max(
+          most, paged_layout(total_q, seqs, H, Hk, D, fp4_shape(group, len, seqs)).total);
+  }
+  if (group * max_seqlen > kFp4RowsMost) most += fp4_pages(B, Hk, D, max_kv_len).total;
+  return most;
+}
+
+// Whether every bf16 page of the batch has a number.
+bool fp4_pages_ok(int32_t B, int32_t max_kv_len) {
+  return (static_cast<int64_t>(max_kv_len) / kFp4OutPage + 1) * B < kInt31;
+}
+
+// A cache's power of two, 2^-32 to 2^32: codes times scales times it stay exact in bf16.
+bool unit_ok(float u) {
+  int e;
+  return std::isfinite(u) && std::frexp(u, &e) == 0.5f && e >= -31 && e <= 33;
+}
+
+// The 4-bit cache's own arguments.
+int check_fp4(int64_t num_pages, int32_t page_size, int64_t page_stride, int32_t max_pages,
+              int32_t Hk, int32_t D, float k_scale, float v_scale) {
+  if (D != 64 && D != 128) return CPATTN_ERR_UNSUPPORTED;
+  if (page_shift_of(page_size) < 0) return CPATTN_ERR_UNSUPPORTED;
+  if (Hk < 1 || Hk > 65535 || num_pages < 1 || num_pages >= kInt31 || max_pages < 0 ||
+      page_stride < static_cast<int64_t>(page_size) * Hk * 9 * D / 16 || page_stride % 16 != 0)
+    return CPATTN_ERR_INVALID_ARG;
+  if (!unit_ok(k_scale) || !unit_ok(v_scale)) return CPATTN_ERR_INVALID_ARG;
+  return CPATTN_OK;
+}
+
+bool fp4_caches_ok(const void* k_cache, const void* v_cache) {
+  return k_cache != nullptr && v_cache != nullptr && aligned(k_cache, 16) &&
+         aligned(v_cache, 16) && k_cache != v_cache;
+}
+
+bool ints_ok(const void* p) { return p != nullptr && aligned(p, 4); }
 
 bool paged_sizes_ok(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t max_seqlen) {
   if (total_q < 0 || total_q >= kInt31 || B < 0 || H < 1 || H > 65535 || Hk < 1 || H % Hk != 0 ||
@@ -482,26 +596,7 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.hdr = reinterpret_cast<WsHeader*>(ws);
-  p.first = reinterpret_cast<int*>(ws + lay.first_off);
-  p.work = reinterpret_cast<PagedWork*>(ws + lay.work_off);
-  p.merge = reinterpret_cast<PagedMerge*>(ws + lay.merge_off);
-  p.arrived = reinterpret_cast<int*>(ws + lay.arrived_off);
-  p.cta_error = reinterpret_cast<int*>(ws + lay.error_off);
-  p.o_part = reinterpret_cast<float*>(ws + lay.o_off);
-  p.lse_part = reinterpret_cast<float*>(ws + lay.lse_off);
-  // The grid: no more splits than units, nor (a plan's items are at most num_seqs)
-  // than one round when they are made to fit one.  CTAs without work cost a small
-  // step a round of their own.
-  p.max_work = lay.max_work;
-  const int64_t units = (static_cast<int64_t>(max_kv_len) + p.shape.unit - 1) / p.shape.unit;
-  const int64_t items = total_q * group / p.shape.rows + num_seqs;
-  if (units < 1) p.max_work = p.max_work < items ? p.max_work : items;
-  else if (p.max_work / units >= items) p.max_work = items * units;
-  const int64_t lanes = static_cast<int64_t>(num_seqs) * num_kv_heads;
-  if (p.shape.plan && 2 * lanes <= p.shape.round && p.max_work > p.shape.round / num_kv_heads)
-    p.max_work = p.shape.round / num_kv_heads;
-  p.max_slots = lay.max_slots;
+  set_workspace(p, ws, lay);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Without rows there is still the error word to write.
   if ((!p.shape.plan || !any) && launch_paged_schedule(p, s) != cudaSuccess)
@@ -518,9 +613,223 @@ extern "C" int cpattn_paged_attn(const void* q, const void* k_cache, const void*
   } else if (launch_paged_rows(p, head_dim, s) != cudaSuccess) {
     return CPATTN_ERR_CUDA;
   }
-  // Lists of short items are never cut; after a plan the merge also writes the error word.
-  if (!p.shape.join && (p.shape.plan || max_kv_len > p.shape.keep * p.shape.unit) &&
-      launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
+  if (merges(p) && launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
+    return CPATTN_ERR_CUDA;
+  return CPATTN_OK;
+}
+
+extern "C" int cpattn_paged_append_fp4(
+    const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* k_cache,
+    void* v_cache, int64_t num_pages, int32_t page_size, int64_t page_stride,
+    const int32_t* page_table, int32_t max_pages, const int32_t* cu_seqlens,
+    const int32_t* kv_lens, int32_t num_seqs, int64_t total_tokens, int32_t num_kv_heads,
+    int32_t head_dim, float k_scale, float v_scale, int32_t* status, void* stream) {
+  int st = check_fp4(num_pages, page_size, page_stride, max_pages, num_kv_heads, head_dim, k_scale,
+                     v_scale);
+  if (st != CPATTN_OK) return st;
+  if (num_seqs < 0 || !counts_ok(total_tokens, num_kv_heads)) return CPATTN_ERR_INVALID_ARG;
+  if (status != nullptr && !aligned(status, 4)) return CPATTN_ERR_INVALID_ARG;
+  if (total_tokens == 0 || num_seqs == 0) return CPATTN_OK;
+  if (!rows_ok(k, k_stride, num_kv_heads, head_dim) ||
+      !rows_ok(v, v_stride, num_kv_heads, head_dim) || !fp4_caches_ok(k_cache, v_cache) ||
+      !ints_ok(page_table) || !ints_ok(cu_seqlens) || !ints_ok(kv_lens))
+    return CPATTN_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = serve_device(&dev);
+  if (st != CPATTN_OK) return st;
+  Fp4CacheParams p{};
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.page_table = page_table;
+  p.num_seqs = num_seqs;
+  p.num_pages = static_cast<int>(num_pages);
+  p.page_shift = page_shift_of(page_size);
+  p.max_pages = max_pages;
+  p.kv_heads = num_kv_heads;
+  p.page_stride = page_stride;
+  p.total_tokens = total_tokens;
+  p.k_scale = 1.f / k_scale;
+  p.v_scale = 1.f / v_scale;
+  p.status = status;
+  return launch_fp4_append(p, head_dim, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CPATTN_OK
+             : CPATTN_ERR_CUDA;
+}
+
+extern "C" int cpattn_paged_gather_fp4(
+    const void* k_cache, const void* v_cache, int64_t num_pages, int32_t page_size,
+    int64_t page_stride, const int32_t* page_table, int32_t max_pages, const int32_t* cu_seqlens,
+    const int32_t* kv_lens, int32_t num_seqs, int64_t total_tokens, int32_t num_kv_heads,
+    int32_t head_dim, float k_scale, float v_scale, void* k_out, int64_t k_stride, void* v_out,
+    int64_t v_stride, int32_t* status, void* stream) {
+  int st = check_fp4(num_pages, page_size, page_stride, max_pages, num_kv_heads, head_dim, k_scale,
+                     v_scale);
+  if (st != CPATTN_OK) return st;
+  if (num_seqs < 0 || !counts_ok(total_tokens, num_kv_heads)) return CPATTN_ERR_INVALID_ARG;
+  if (status != nullptr && !aligned(status, 4)) return CPATTN_ERR_INVALID_ARG;
+  if (total_tokens == 0 || num_seqs == 0) return CPATTN_OK;
+  if (!rows_ok(k_out, k_stride, num_kv_heads, head_dim) ||
+      !rows_ok(v_out, v_stride, num_kv_heads, head_dim) || k_out == v_out ||
+      !fp4_caches_ok(k_cache, v_cache) || !ints_ok(page_table) || !ints_ok(cu_seqlens) ||
+      !ints_ok(kv_lens))
+    return CPATTN_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = serve_device(&dev);
+  if (st != CPATTN_OK) return st;
+  Fp4CacheParams p{};
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.k_cache = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+  p.v_cache = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.page_table = page_table;
+  p.num_seqs = num_seqs;
+  p.num_pages = static_cast<int>(num_pages);
+  p.page_shift = page_shift_of(page_size);
+  p.max_pages = max_pages;
+  p.kv_heads = num_kv_heads;
+  p.page_stride = page_stride;
+  p.total_tokens = total_tokens;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.status = status;
+  return launch_fp4_gather(p, head_dim, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CPATTN_OK
+             : CPATTN_ERR_CUDA;
+}
+
+extern "C" size_t cpattn_paged_attn_fp4_workspace_size(int64_t total_q, int32_t num_seqs,
+                                                       int32_t num_heads, int32_t num_kv_heads,
+                                                       int32_t head_dim, int32_t max_seqlen,
+                                                       int32_t max_kv_len) {
+  if (!paged_sizes_ok(total_q, num_seqs, num_heads, num_kv_heads, max_seqlen) ||
+      (head_dim != 64 && head_dim != 128) || num_heads / num_kv_heads > kPagedMaxGroup ||
+      max_kv_len < 0 || max_kv_len > (1 << 30) || !fp4_pages_ok(num_seqs, max_kv_len))
+    return 0;
+  return fp4_workspace(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
+                       max_kv_len);
+}
+
+extern "C" int cpattn_paged_attn_fp4(
+    const void* q, const void* k_cache, const void* v_cache, int64_t num_pages,
+    int32_t page_size, int64_t page_stride, const int32_t* page_table, int32_t max_pages,
+    const int32_t* cu_seqlens, const int32_t* kv_lens, int32_t num_seqs, int64_t total_q,
+    int32_t max_seqlen, int32_t max_kv_len, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, float k_scale, float v_scale, float softmax_scale, int32_t causal, void* out,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_fp4(num_pages, page_size, page_stride, max_pages, num_kv_heads, head_dim, k_scale,
+                     v_scale);
+  if (st != CPATTN_OK) return st;
+  if (!paged_sizes_ok(total_q, num_seqs, num_heads, num_kv_heads, max_seqlen) || max_kv_len < 0 ||
+      max_kv_len > (1 << 30))
+    return CPATTN_ERR_INVALID_ARG;
+  const int group = num_heads / num_kv_heads;
+  if (group > kPagedMaxGroup || !fp4_pages_ok(num_seqs, max_kv_len)) return CPATTN_ERR_UNSUPPORTED;
+  if (!(std::isfinite(softmax_scale) && softmax_scale > 0.f) || (causal != 0 && causal != 1))
+    return CPATTN_ERR_INVALID_ARG;
+  const float scale_log2 = softmax_scale * 1.4426950408889634f * k_scale;
+  if (!std::isnormal(scale_log2)) return CPATTN_ERR_INVALID_ARG;
+  const bool any = total_q > 0 && num_seqs > 0;
+  if (any) {
+    if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16) || out == q ||
+        !fp4_caches_ok(k_cache, v_cache) || max_seqlen < 1)
+      return CPATTN_ERR_INVALID_ARG;
+    // A batch without cached keys may come without a table.
+    if (max_pages > 0 && !ints_ok(page_table)) return CPATTN_ERR_INVALID_ARG;
+  }
+  if (num_seqs > 0 && (!ints_ok(cu_seqlens) || !ints_ok(kv_lens))) return CPATTN_ERR_INVALID_ARG;
+  if (lse != nullptr && !aligned(lse, 4)) return CPATTN_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, kServeAlign)) return CPATTN_ERR_INVALID_ARG;
+  Fp4RowsParams f{};
+  PagedParams& p = f.p;
+  p.shape = fp4_shape(group, max_seqlen, num_seqs);
+  const PagedLayout lay =
+      paged_layout(total_q, num_seqs, num_heads, num_kv_heads, head_dim, p.shape);
+  Fp4Pages pages{};
+  if (p.shape.tiles) pages = fp4_pages(num_seqs, num_kv_heads, head_dim, max_kv_len);
+  if (workspace_bytes < lay.total + pages.total) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  if (lay.max_work * num_kv_heads >= kInt31) return CPATTN_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  st = serve_device(&dev);
+  if (st != CPATTN_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.page_table = page_table;
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.num_pages = static_cast<int>(num_pages);
+  p.page_shift = page_shift_of(page_size);
+  p.max_pages = max_pages;
+  p.causal = causal;
+  p.max_seqlen = max_seqlen;
+  p.max_kv_len = max_kv_len;
+  p.total_q = total_q;
+  p.scale_log2 = scale_log2;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  set_workspace(p, ws, lay);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Without rows there is still the error word to write.
+  if ((!p.shape.plan || !any) && launch_paged_schedule(p, s) != cudaSuccess)
+    return CPATTN_ERR_CUDA;
+  if (!any) return CPATTN_OK;
+  if (p.shape.tiles) {
+    // Their page table, pages and strides take the place of the caches'.
+    Fp4PagesParams g{};
+    g.k_cache = static_cast<const uint8_t*>(k_cache);
+    g.v_cache = static_cast<const uint8_t*>(v_cache);
+    g.out_table = reinterpret_cast<int*>(ws + lay.total);
+    g.k_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.total + pages.k_off);
+    g.v_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.total + pages.v_off);
+    g.kv_lens = kv_lens;
+    g.page_table = page_table;
+    g.num_seqs = num_seqs;
+    g.num_pages = p.num_pages;
+    g.page_shift = p.page_shift;
+    g.max_pages = max_pages;
+    g.kv_heads = num_kv_heads;
+    g.out_pages = static_cast<int>(pages.pages);
+    g.max_kv_len = max_kv_len;
+    g.page_stride = page_stride;
+    g.v_scale = v_scale;
+    g.hdr = p.hdr;
+    if (pages.pages > 0 && launch_fp4_pages(g, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+    p.k_cache = g.k_out;
+    p.v_cache = g.v_out;
+    p.page_table = g.out_table;
+    p.max_pages = g.out_pages;
+    p.num_pages = num_seqs * g.out_pages;
+    p.page_shift = page_shift_of(kFp4OutPage);
+    p.page_stride = static_cast<int64_t>(kFp4OutPage) * num_kv_heads * head_dim;
+    if (pages.pages == 0) p.num_pages = 1;  // no key: the maps need some extent
+    CUtensorMap tq, tk, tv, to;
+    if (q_tile_map(&tq, q, p, head_dim) != CPATTN_OK ||
+        q_tile_map(&to, out, p, head_dim) != CPATTN_OK ||
+        cache_map(&tk, p.k_cache, p, head_dim) != CPATTN_OK ||
+        cache_map(&tv, p.v_cache, p, head_dim) != CPATTN_OK)
+      return CPATTN_ERR_CUDA;
+    if (launch_paged_tile(tq, tk, tv, to, p, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+  } else {
+    f.k_cache = static_cast<const uint8_t*>(k_cache);
+    f.v_cache = static_cast<const uint8_t*>(v_cache);
+    f.page_stride = page_stride;
+    f.v_scale = v_scale;
+    if (launch_fp4_rows(f, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+  }
+  if (merges(p) && launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   return CPATTN_OK;
 }

@@ -45,7 +45,8 @@ Modules:
   definition in ``include/cpattn.h``).
 * :mod:`oracle.paged`     -- the paged KV cache: where a token stands, and
   attention of new tokens over it (likewise).
+* :mod:`oracle.paged_fp4` -- the 4-bit cache's format and rounding (likewise).
 """
 
-from . import (attention, backward, dcp, decode, norm_rope, paged, planner,  # noqa: F401
-               ulysses)
+from . import (attention, backward, dcp, decode, norm_rope, paged, paged_fp4,  # noqa: F401
+               planner, ulysses)
