@@ -30,6 +30,8 @@
 // 11 bits down to 2^-25 of the largest weight.  l sums p in fp32.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "kernels.h"
 #include "paged_plan.cuh"
@@ -44,44 +46,33 @@ constexpr int kF4RowsThreads = kF4Warps * 32;
 constexpr float kNegInfF = -__builtin_huge_valf();
 constexpr float kLn2F = 0.69314718055994530942f;
 constexpr float kLog2eF = 1.44269504088896340736f;
-constexpr float kMoveByF = 4.f;  // powers of two
-constexpr float kLiftF = 11.f;   // powers of two of the largest weight
+constexpr float kLiftF = 11.f;       // powers of two of a weight at the reference
+constexpr float kMaxSumF = 32768.f;  // of a lane's weights of a row in one pass
 
 enum : int { kErrArgF4 = 1, kErrTimeoutF4 = 6 };
 
+#ifndef F4_T1
+#define F4_T1 4
+#define F4_S1 2
+#define F4_C1 3
+#define F4_P1 4
+#endif
 template <int D, int NT>
 struct Fp4RowsCfg {
-  static constexpr int kTiles = D == 128 ? 2 : 4;  // tiles of a step
+  static constexpr int kTiles = (D == 128 ? 1 : 2) * (NT == 1 ? F4_T1 : 2);  // tiles of a step
   static constexpr int kKeys = kTiles * kFp4Tile;
   static constexpr int kHalf = kTiles * Fp4<D>::kTileBytes;  // K (or V) of a step
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 3;
-  static constexpr int kRing = kF4Warps * kStages * kStage;  // 55 KB
+  static constexpr int kStages = NT == 1 ? F4_S1 : 3;
+  static constexpr int kRing = kF4Warps * kStages * kStage;
   static constexpr int kRows = 8 * NT;
   static constexpr int kJoin = kF4Warps * kRows * D * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
   // Tiles whose scores are taken together.
-  static constexpr int kPass = NT == 4 ? (D == 128 ? 1 : 2) : 2;
-  static constexpr int kCtas = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // of an SM
+  static constexpr int kPass = NT == 1 ? F4_P1 : (NT == 4 ? (D == 128 ? 1 : 2) : 2);
+  static constexpr int kCtas = NT == 1 ? F4_C1 : (NT == 2 ? 3 : 2);  // of an SM
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts128_zero(uint32_t a) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
 }
@@ -141,29 +132,10 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   const int row0 = all_rows - (n_blk - blk) * kRows;
 
   // Steps of this warp: keys [kv_lo + (warp + 4 i) kKeys, + kKeys).
-  const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;
-  const int page_tiles = 1 << (p.page_shift - 4);
   const int all_steps = (kv_hi - kv_lo + C::kKeys - 1) / C::kKeys;
   const int steps = all_steps > warp ? (all_steps - warp + kF4Warps - 1) / kF4Warps : 0;
-  auto step_key = [&](int i) { return kv_lo + (warp + i * kF4Warps) * C::kKeys; };
-  auto step_tiles = [&](int i) {
-    return min(C::kTiles, (kv_hi - step_key(i) + kFp4Tile - 1) / kFp4Tile);
-  };
   const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
   uint64_t* full = s_full[warp];
-  // A step's tiles come in runs that share a page; lane 2 r copies run r of K, lane
-  // 2 r + 1 of V.  Its page number is read a step ahead.
-  const int run_tiles = min(C::kTiles, page_tiles);
-  const int run_at = (lane >> 1) * run_tiles;
-  const uint8_t* cache = (lane & 1) ? fp.v_cache : fp.k_cache;
-  const size_t head_at = static_cast<size_t>(h) * page_tiles * F::kTileBytes;
-  auto page_of = [&](int i) {
-    return i < steps && run_at < step_tiles(i)
-               ? __ldg(pages + ((step_key(i) + run_at * kFp4Tile) >> p.page_shift))
-               : 0;
-  };
-  int next_page = page_of(0);
-  bool bad_page = false;
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
@@ -171,43 +143,64 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   }
   if (threadIdx.x == 0) s_abort = 0;
   __syncthreads();
-  auto copy = [&](int i) {
-    if (i >= steps) return;
-    const int page = next_page;
-    next_page = page_of(i + 1);
-    const int st = i % C::kStages;
-    const int n = min(run_tiles, step_tiles(i) - run_at);  // tiles of this lane's run
-    const bool have = n > 0 && lane < 2 * C::kTiles;
-    const bool good = have && page >= 0 && page < p.num_pages;
-    const uint32_t bytes = good ? n * F::kTileBytes : 0;
-    const uint32_t dst = ring + st * C::kStage + (lane & 1) * C::kHalf + run_at * F::kTileBytes;
-    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
-    if (lane == 0) mbar_arrive_expect_tx(full + st, all);
-    __syncwarp();
+  // A step's tiles come in runs that share a page; lane 2 r copies run r of K, lane
+  // 2 r + 1 of V.  Its page number is read a step ahead.
+  const int page_tiles = 1 << (p.page_shift - 4);
+  const int run_tiles = min(C::kTiles, page_tiles);
+  const int run_at = (lane >> 1) * run_tiles;
+  const int copy_end = run_at < C::kTiles ? kv_hi : 0;
+  const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;
+  const uint8_t* cache = ((lane & 1) ? fp.v_cache : fp.k_cache) +
+                         static_cast<size_t>(h) * page_tiles * F::kTileBytes;
+  int copy_key = kv_lo + warp * C::kKeys + run_at * kFp4Tile;  // of the next copy
+  uint32_t copy_to = ring + (lane & 1) * C::kHalf + run_at * F::kTileBytes;
+  uint32_t copy_bar = smem_u32(full);
+  int copy_left = steps;
+  int next_page = copy_key < copy_end ? __ldg(pages + (copy_key >> p.page_shift)) : 0;
+  bool bad_page = false;
+  auto copy = [&]() {
+    if (copy_left <= 0) return;
+    --copy_left;
+    const int page = next_page, key = copy_key;
+    copy_key += kF4Warps * C::kKeys;
+    if (copy_key < copy_end) next_page = __ldg(pages + (copy_key >> p.page_shift));
 #ifdef CPATTN_FAULT_INJECT_DROP_P
-    if (blockIdx.x == 0 && warp == 0 && i == 0) return;
+    const bool drop = blockIdx.x == 0 && warp == 0 && copy_left == steps - 1;
+#else
+    constexpr bool drop = false;
 #endif
-    if (good) {
-      const int at = ((step_key(i) + run_at * kFp4Tile) >> 4) & (page_tiles - 1);
-      bulk_load(dst, cache + static_cast<size_t>(page) * fp.page_stride + head_at +
-                         static_cast<size_t>(at) * F::kTileBytes,
-                bytes, full + st);
-    } else if (have) {
-      // Its keys or values count as zeros: their scales are.
-      bad_page = true;
-      for (int x = 0; x < n; ++x)
-        for (int y = 0; y < D; y += 16) sts128_zero(dst + x * F::kTileBytes + F::kScales + y);
-      fence_proxy_async_smem();
+    if (key < copy_end) {
+      const int n = min(run_tiles, (copy_end - key + kFp4Tile - 1) / kFp4Tile);
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
+        const int at = (key >> 4) & (page_tiles - 1);
+        const uint32_t bytes = n * F::kTileBytes;
+        mbar_expect_tx(copy_bar, bytes);
+        if (!drop)
+          bulk_load(copy_to, cache + static_cast<size_t>(page) * fp.page_stride + at * F::kTileBytes,
+                    bytes, copy_bar);
+      } else {
+        // Its keys or values count as zeros: their scales are.
+        bad_page = true;
+        for (int x = 0; x < n; ++x)
+          for (int y = 0; y < D; y += 16)
+            sts128_zero(copy_to + x * F::kTileBytes + F::kScales + y);
+        fence_proxy_async_smem();
+      }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(copy_bar);
+    const bool wrap = copy_bar == smem_u32(full + C::kStages - 1);
+    copy_to += wrap ? (1 - C::kStages) * C::kStage : C::kStage;
+    copy_bar += wrap ? (1 - C::kStages) * 8 : 8;
   };
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) copy(i);
+  for (int i = 0; i < C::kStages - 1; ++i) copy();
 
   // The queries as right operands: lane (g, t) has row g of each block of eight,
   // features [t D / 4, + D / 4), as fp16 times a power of two that brings the row's
   // largest below 2^15.
   uint32_t q[NT][kM][2];
-  float sc[NT][2];  // from a score to the exponent, rows 2 t and 2 t + 1
+  float2 sc[NT];    // from a score to the exponent, rows 2 t and 2 t + 1
   int lim[NT][2];   // keys below it are visible
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -245,63 +238,57 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // A normal number: masked scores (-inf) and zeros are multiplied by it.
-      sc[nt][i] = fminf(fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + i) * 4) * p.scale_log2,
-                              1.17549435e-38f), 3.40282347e38f);
+      (i ? sc[nt].y : sc[nt].x) =
+          fminf(fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + i) * 4) * p.scale_log2,
+                      1.17549435e-38f), 3.40282347e38f);
       const int r = row0 + nt * 8 + 2 * t + i;
-      lim[nt][i] = r < 0 ? 0 : (p.causal ? kv_len - q_len + r / G + 1 : kv_len);
+      lim[nt][i] = p.causal && r >= 0 ? kv_len - q_len + r / G + 1 : kv_len;
     }
   }
-  // Steps ending at or below this key need no mask (rows are in order, so the
-  // block's first row sees the fewest keys).
-  const int first_tok = max(row0, 0) / G;
-  const int free_end = row0 < 0 ? 0 : (p.causal ? kv_len - q_len + first_tok + 1 : kv_len);
+  // Steps ending at or below this key need no mask (rows are in order, so the block's
+  // first row sees the fewest keys; what rows that are not there see does not matter).
+  const int free_end = p.causal ? kv_len - q_len + max(row0, 0) / G + 1 : kv_len;
 
   // Lane (g, t) accumulates rows 2 t and 2 t + 1 of features g D / 8 + 2 i and + 1, i
   // below D / 16: [i][feature][row] with permuted pairs, else [i / 2][feature][i % 2][row].
   float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
+  float m[NT][2];          // the references
+  float2 off[NT], l[NT];   // 11 - m (11 without a reference) and the sums, by rows
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt][0] = m[nt][1] = kNegInfF;
-    l[nt][0] = l[nt][1] = 0.f;
+    off[nt] = make_float2(kLiftF, kLiftF);
+    l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[nt][i][x] = 0.f;
   }
+  bool fresh = true;  // some row has no reference yet
 
   bool failed = false;
-  int step = 0;
-#pragma unroll 1
-  for (; step < steps; ++step) {
-    const int st = step % C::kStages;
-    const bool landed = wait_bounded(full + st, (step / C::kStages) & 1, &s_abort);
-    if (__any_sync(0xffffffffu, !landed)) {
-      failed = true;
-      break;
-    }
-    copy(step + C::kStages - 1);
-    const int key0 = step_key(step);
-    const int tiles = step_tiles(step);
-    const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
+  int step = 0, st = 0, key0 = kv_lo + warp * C::kKeys;
+  uint32_t parity = 0;
+  const int k_at = t * (D / 64);           // first group of this lane's keys
+  const int v_at = D == 128 ? g : g >> 1;  // group of its values
+  // One step.  kWhole: all of its keys are there and every row sees them.
+  auto take = [&](auto whole, const uint8_t* stage, int left) {
+    constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
     for (int pass = 0; pass < C::kTiles; pass += C::kPass) {
-      if (pass > 0 && pass >= tiles) break;
+      if (!kWhole && pass > 0 && pass * kFp4Tile >= left) break;
       float s[C::kPass][NT][4];
 #pragma unroll
       for (int u = 0; u < C::kPass; ++u) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[u][nt][x] = 0.f;
-        if (u > 0 && pass + u >= tiles) continue;
+        // (A tile behind the split's end holds what an earlier step left.)
         // Rows of the left operand: token 2 g, and 2 g + 1 as row g + 8.
-        const uint32_t tile = kb + (pass + u) * F::kTileBytes;
+        const uint8_t* tile = stage + (pass + u) * F::kTileBytes;
 #pragma unroll
         for (int gg = 0; gg < D / 64; ++gg) {
-          const int j = t * (D / 64) + gg;
-          const uint4 k4 = lds128(tile + F::place(j, g));
-          const uint32_t both = e4m3x2_to_f16(lds16(tile + F::kScales + j * kFp4Tile + 2 * g));
+          const int j = k_at + gg;
+          const uint4 k4 = *reinterpret_cast<const uint4*>(tile + F::place(j, g));
+          const uint32_t both = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(
+              tile + F::kScales + j * kFp4Tile + 2 * g));
           const uint32_t s0 = __byte_perm(both, 0, 0x1010), s1 = __byte_perm(both, 0, 0x3232);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -318,12 +305,15 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
               const uint32_t op[4] = {a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1]};
               const int mm = gg * 4 + half * 2 + i;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_16816_f16(s[u][nt], op, q[nt][mm][0], q[nt][mm][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                if (mm == 0) mma_16816_f16_first(s[u][nt], op, q[nt][mm][0], q[nt][mm][1]);
+                else mma_16816_f16(s[u][nt], op, q[nt][mm][0], q[nt][mm][1]);
             }
           }
         }
       }
-      if (key0 + (pass + C::kPass) * kFp4Tile > free_end || pass + C::kPass > tiles) {
+      const int pass_end = (pass + C::kPass) * kFp4Tile;
+      if (!kWhole && (key0 + pass_end > free_end || pass_end > left)) {
 #pragma unroll
         for (int u = 0; u < C::kPass; ++u)
 #pragma unroll
@@ -334,31 +324,54 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
               if (key >= lim[nt][x & 1] || key >= kv_hi) s[u][nt][x] = kNegInfF;
           }
       }
-      bool move = false;
-      float top[NT][2];
+      // The exponentials against the references as they are; again, against new ones,
+      // if a lane's sum leaves fp16's range or a row has none yet.
+      float2 e2[C::kPass][NT][2], sum[NT];
+      auto exponentials = [&] {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          sum[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float v = kNegInfF;
+          for (int u = 0; u < C::kPass; ++u)
 #pragma unroll
-          for (int u = 0; u < C::kPass; ++u) v = fmax3(v, s[u][nt][i], s[u][nt][i + 2]);
-          top[nt][i] = v * sc[nt][i];
-          move = move || top[nt][i] > m[nt][i] + kMoveByF;
+            for (int y = 0; y < 2; ++y) {
+              const float2 x = __ffma2_rn(make_float2(s[u][nt][2 * y], s[u][nt][2 * y + 1]), sc[nt],
+                                          off[nt]);
+              e2[u][nt][y] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              sum[nt] = __fadd2_rn(sum[nt], e2[u][nt][y]);
+            }
         }
-      if (__any_sync(0xffffffffu, move)) {
+      };
+#pragma unroll 1
+      for (int round = 0;; ++round) {
+        exponentials();
+        if (round > 0) break;
+        bool move = fresh;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          move = move || !(sum[nt].x <= kMaxSumF) || !(sum[nt].y <= kMaxSumF);
+        if (!__any_sync(0xffffffffu, move)) break;
+        fresh = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float v = top[nt][i];
+            float v = kNegInfF;
+#pragma unroll
+            for (int u = 0; u < C::kPass; ++u) v = fmax3(v, s[u][nt][i], s[u][nt][i + 2]);
+            v *= i ? sc[nt].y : sc[nt].x;
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             const float mn = fmaxf(m[nt][i], v);
             const float alpha = m[nt][i] == kNegInfF ? 0.f : ex2_approx(m[nt][i] - mn);
             m[nt][i] = mn;
-            l[nt][i] *= alpha;
+            const float to = mn == kNegInfF ? kLiftF : kLiftF - mn;
+            if (i) off[nt].y = to;
+            else off[nt].x = to;
+            if (i) l[nt].y *= alpha;
+            else l[nt].x *= alpha;
+            fresh = fresh || mn == kNegInfF;
 #pragma unroll
             for (int f = 0; f < D / 16; ++f) {
               o[nt][f][i] *= alpha;
@@ -367,33 +380,25 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
           }
       }
 #pragma unroll
+      for (int nt = 0; nt < NT; ++nt) l[nt] = __fadd2_rn(l[nt], sum[nt]);
+#pragma unroll
       for (int u = 0; u < C::kPass; ++u) {
-        if (u > 0 && pass + u >= tiles) continue;
+        if (!kWhole && u > 0 && (pass + u) * kFp4Tile >= left) break;
         // P of this lane's row g: pa tokens 4 t and 4 t + 2, pb 4 t + 1 and 4 t + 3.
         uint32_t pa[NT], pb[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float e2[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float mr = m[nt][x & 1];
-            const float off = mr == kNegInfF ? kLiftF : kLiftF - mr;
-            e2[x] = ex2_approx(fmaf(s[u][nt][x], sc[nt][x & 1], off));
-          }
-          l[nt][0] += e2[0] + e2[2];
-          l[nt][1] += e2[1] + e2[3];
-          pa[nt] = transpose_8x8(pack_f16x2(e2[0], e2[1]));
-          pb[nt] = transpose_8x8(pack_f16x2(e2[2], e2[3]));
+          pa[nt] = transpose_8x8(pack_f16x2(e2[u][nt][0].x, e2[u][nt][0].y));
+          pb[nt] = transpose_8x8(pack_f16x2(e2[u][nt][1].x, e2[u][nt][1].y));
         }
-        const uint32_t tile = vb + (pass + u) * F::kTileBytes;
-        const int j = D == 128 ? g : g >> 1;
-        const uint4 v01 = lds128(tile + F::place(j, 2 * t));
-        const uint4 v23 = lds128(tile + F::place(j, 2 * t + 1));
-        uint32_t sb = lds32(tile + F::kScales + j * kFp4Tile + 4 * t);
+        const uint8_t* tile = stage + C::kHalf + (pass + u) * F::kTileBytes;
+        const uint4 v01 = *reinterpret_cast<const uint4*>(tile + F::place(v_at, 2 * t));
+        const uint4 v23 = *reinterpret_cast<const uint4*>(tile + F::place(v_at, 2 * t + 1));
+        uint32_t sb =
+            *reinterpret_cast<const uint32_t*>(tile + F::kScales + v_at * kFp4Tile + 4 * t);
         // What lies behind the cache's end has weight 0, and a NaN there is one.
-        const int left = kv_len - (key0 + (pass + u) * kFp4Tile);
-        if (left < kFp4Tile) {
-          const int n = left - 4 * t;
+        if (!kWhole && left < (pass + u + 1) * kFp4Tile) {
+          const int n = kv_len - (key0 + (pass + u) * kFp4Tile) - 4 * t;
           sb = n <= 0 ? 0u : (n >= 4 ? sb : sb & ((1u << (8 * n)) - 1u));
         }
         const uint32_t s01 = e4m3x2_to_f16(sb), s23 = e4m3x2_to_f16(sb >> 16);
@@ -463,6 +468,23 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
         }
       }
     }
+  };
+
+#pragma unroll 1
+  for (; step < steps; ++step) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait_sleep(full + st, parity, kWaitSleepNs)) &&
+        __any_sync(0xffffffffu, !wait_bounded(full + st, parity, &s_abort))) {
+      failed = true;
+      break;
+    }
+    copy();
+    const uint8_t* stage = smem + warp * (C::kStages * C::kStage) + st * C::kStage;
+    const int left = kv_hi - key0;  // keys of the split from here on
+    if (key0 + C::kKeys <= free_end && left >= C::kKeys) take(std::true_type(), stage, left);
+    else take(std::false_type(), stage, left);
+    key0 += kF4Warps * C::kKeys;
+    st = st + 1 == C::kStages ? 0 : st + 1;
+    parity ^= st == 0;
     __syncwarp();  // the stage may be filled again
   }
   if (failed) {
@@ -470,9 +492,10 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     // Copies in flight still write to this CTA's memory.
     for (int i = step; i < min(steps, step + C::kStages - 1); ++i) {
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(full + i % C::kStages, (i / C::kStages) & 1) &&
-             global_timer_ns() - t0 < 200000000ull) {
+      while (!mbar_try_wait(full + st, parity) && global_timer_ns() - t0 < 200000000ull) {
       }
+      st = st + 1 == C::kStages ? 0 : st + 1;
+      parity ^= st == 0;
     }
   }
 
@@ -490,7 +513,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = nt * 8 + 2 * t + i;
-      float sum = l[nt][i];
+      float sum = i ? l[nt].y : l[nt].x;
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);

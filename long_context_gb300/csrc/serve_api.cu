@@ -202,8 +202,14 @@ PagedShape fp4_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   s.unit = 64;
   s.min_units = 24;
   s.whole = s.keep = 1;
-  s.ctas = 608;
-  s.round = 152 * (rows <= 8 ? 4 : (rows <= 16 ? 3 : 2));  // CTAs that an SM holds
+#ifndef F4_CT
+#define F4_CT 608
+#endif
+  s.ctas = F4_CT;
+#ifndef F4_C1
+#define F4_C1 3
+#endif
+  s.round = 152 * (rows <= 8 ? F4_C1 : (rows <= 16 ? 3 : 2));  // CTAs that an SM holds
   return s;
 }
 
