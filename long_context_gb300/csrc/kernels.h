@@ -376,6 +376,7 @@ struct Fp4RowsParams {
   const uint8_t *k_cache, *v_cache;
   long long page_stride;
   float v_scale;                     // (p.scale_log2 has the keys')
+  int parts;                         // > 0: so many CTAs to a sequence and KV head, no list
 };
 
 cudaError_t launch_fp4_rows(const Fp4RowsParams& p, int D, cudaStream_t stream);

@@ -23,7 +23,10 @@ namespace cpattn {
 namespace {
 
 constexpr int kF4Threads = 256;
-constexpr int kF4Run = 4;  // heads of a unit
+#ifndef F4_RUN
+#define F4_RUN 4
+#endif
+constexpr int kF4Run = F4_RUN;  // heads of a unit
 constexpr int kErrArgF = 1;  // CPATTN_ERR_INVALID_ARG
 
 // Place of a new token: its tile's first byte in head 0 of its page, or -1.

@@ -49,28 +49,30 @@ constexpr float kLog2eF = 1.44269504088896340736f;
 constexpr float kLiftF = 11.f;       // powers of two of a weight at the reference
 constexpr float kMaxSumF = 32768.f;  // of a lane's weights of a row in one pass
 
+constexpr int kF4MaxParts = 8;       // CTAs of a portable cluster
+
 enum : int { kErrArgF4 = 1, kErrTimeoutF4 = 6 };
 
-#ifndef F4_T1
-#define F4_T1 4
-#define F4_S1 2
-#define F4_C1 3
-#define F4_P1 4
-#endif
+// Where a CTA's work comes from.
+enum class Fp4Work {
+  kList,   // the schedule kernel's list
+  kPlan,   // worked out by every warp (paged_plan.cuh)
+  kStatic  // a cluster of CTAs has one sequence and KV head, in equal parts
+};
+
 template <int D, int NT>
 struct Fp4RowsCfg {
-  static constexpr int kTiles = (D == 128 ? 1 : 2) * (NT == 1 ? F4_T1 : 2);  // tiles of a step
+  static constexpr int kTiles = (NT == 1 ? 4 : 2) * (128 / D);  // tiles of a step
   static constexpr int kKeys = kTiles * kFp4Tile;
   static constexpr int kHalf = kTiles * Fp4<D>::kTileBytes;  // K (or V) of a step
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = NT == 1 ? F4_S1 : 3;
-  static constexpr int kRing = kF4Warps * kStages * kStage;
+  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kRing = kF4Warps * kStages * kStage;  // 74 or 55 KB
   static constexpr int kRows = 8 * NT;
   static constexpr int kJoin = kF4Warps * kRows * D * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-  // Tiles whose scores are taken together.
-  static constexpr int kPass = NT == 1 ? F4_P1 : (NT == 4 ? (D == 128 ? 1 : 2) : 2);
-  static constexpr int kCtas = NT == 1 ? F4_C1 : (NT == 2 ? 3 : 2);  // of an SM
+  static constexpr int kPass = NT == 1 ? 4 : 2;  // tiles whose scores are taken together
+  static constexpr int kCtas = NT == 4 ? 2 : 3;  // of an SM
 };
 
 __device__ __forceinline__ void sts128_zero(uint32_t a) {
@@ -79,28 +81,61 @@ __device__ __forceinline__ void sts128_zero(uint32_t a) {
 
 }  // namespace
 
-template <int D, int NT, bool PLAN>
+template <int D, int NT, Fp4Work W>
 __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     fp4_rows_kernel(const Fp4RowsParams fp) {
   using C = Fp4RowsCfg<D, NT>;
+  constexpr bool kPlan = W == Fp4Work::kPlan;
+  constexpr bool kStatic = W == Fp4Work::kStatic;
   using F = Fp4<D>;
   const PagedParams& p = fp.p;
   constexpr int kRows = C::kRows;
-  constexpr bool kPairs = NT > 1;   // permuted pairs of keys
+  constexpr bool kMany = NT > 1;    // the queries in shared memory, permuted pairs of keys
   constexpr int kM = D / 16;        // products of a tile's scores
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kF4Warps][kRows], s_l[kF4Warps][kRows];
   __shared__ __align__(8) uint64_t s_full[kF4Warps][C::kStages];
+  __shared__ float s_back[kRows];
+  __shared__ int s_lim[kRows];
+  __shared__ uint4 s_q[kMany ? NT * (kM / 2) * 32 : 1];
   __shared__ int s_last, s_abort;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int Hk = p.num_kv_heads, G = p.group;
-  const int e = static_cast<int>(blockIdx.x) / Hk;
-  const int h = static_cast<int>(blockIdx.x) - e * Hk;
+  const int rank = kStatic ? static_cast<int>(blockIdx.x) % fp.parts : 0;
+  const int eh = kStatic ? static_cast<int>(blockIdx.x) / fp.parts : static_cast<int>(blockIdx.x);
+  const int e = eh / Hk;
+  const int h = eh - e * Hk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   PagedWork w;
-  if (PLAN) {
+  if (kStatic) {
+    // Every CTA checks all lengths (as the schedule kernels do) and takes its own.
+    w.seq = e;
+    w.tok0 = __ldg(p.cu_seqlens + e);
+    w.q_len = __ldg(p.cu_seqlens + e + 1) - w.tok0;
+    w.kv_len = __ldg(p.kv_lens + e);
+    bool bad = false;
+    const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
+    for (int b = threadIdx.x; b < p.num_seqs; b += kF4RowsThreads) {
+      const int lo = __ldg(p.cu_seqlens + b), hi = __ldg(p.cu_seqlens + b + 1);
+      const int kv = __ldg(p.kv_lens + b);
+      bad = bad || lo < 0 || hi < lo || hi > p.total_q || hi - lo > p.max_seqlen || kv < 0 ||
+            kv > p.max_kv_len || kv > cap || (b == 0 && lo != 0);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad || w.q_len == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (bad && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = kErrArgF4;
+      return;
+    }
+    const int units = (w.kv_len + p.shape.unit - 1) / p.shape.unit;
+    const int per = (units + fp.parts - 1) / fp.parts * p.shape.unit;
+    w.blk = 0;
+    w.kv_lo = min(rank * per, w.kv_len);
+    w.kv_hi = min(w.kv_lo + per, w.kv_len);
+    w.slot = -1;
+  } else if (kPlan) {
     const PagedPlan plan = make_plan(p, lane);
     if (e >= plan.splits) return;
     w = plan_split(p, plan, e);
@@ -131,8 +166,11 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   const int n_blk = (all_rows + kRows - 1) / kRows;
   const int row0 = all_rows - (n_blk - blk) * kRows;
 
-  // Steps of this warp: keys [kv_lo + (warp + 4 i) kKeys, + kKeys).
-  const int all_steps = (kv_hi - kv_lo + C::kKeys - 1) / C::kKeys;
+  // Steps of this warp: keys [kv_lo + (warp + 4 i) span, + span), the span a step's
+  // kKeys or, in a short split, less, so that all warps have some.
+  int span = C::kKeys;
+  while (span > kFp4Tile && kv_hi - kv_lo <= span * kF4Warps / 2) span /= 2;
+  const int all_steps = (kv_hi - kv_lo + span - 1) / span;
   const int steps = all_steps > warp ? (all_steps - warp + kF4Warps - 1) / kF4Warps : 0;
   const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
   uint64_t* full = s_full[warp];
@@ -146,13 +184,13 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   // A step's tiles come in runs that share a page; lane 2 r copies run r of K, lane
   // 2 r + 1 of V.  Its page number is read a step ahead.
   const int page_tiles = 1 << (p.page_shift - 4);
-  const int run_tiles = min(C::kTiles, page_tiles);
+  const int run_tiles = min(span / kFp4Tile, page_tiles);
   const int run_at = (lane >> 1) * run_tiles;
-  const int copy_end = run_at < C::kTiles ? kv_hi : 0;
+  const int copy_end = run_at * kFp4Tile < span ? kv_hi : 0;
   const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;
   const uint8_t* cache = ((lane & 1) ? fp.v_cache : fp.k_cache) +
                          static_cast<size_t>(h) * page_tiles * F::kTileBytes;
-  int copy_key = kv_lo + warp * C::kKeys + run_at * kFp4Tile;  // of the next copy
+  int copy_key = kv_lo + warp * span + run_at * kFp4Tile;  // of the next copy
   uint32_t copy_to = ring + (lane & 1) * C::kHalf + run_at * F::kTileBytes;
   uint32_t copy_bar = smem_u32(full);
   int copy_left = steps;
@@ -162,7 +200,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     if (copy_left <= 0) return;
     --copy_left;
     const int page = next_page, key = copy_key;
-    copy_key += kF4Warps * C::kKeys;
+    copy_key += kF4Warps * span;
     if (copy_key < copy_end) next_page = __ldg(pages + (copy_key >> p.page_shift));
 #ifdef CPATTN_FAULT_INJECT_DROP_P
     const bool drop = blockIdx.x == 0 && warp == 0 && copy_left == steps - 1;
@@ -198,12 +236,13 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
 
   // The queries as right operands: lane (g, t) has row g of each block of eight,
   // features [t D / 4, + D / 4), as fp16 times a power of two that brings the row's
-  // largest below 2^15.
-  uint32_t q[NT][kM][2];
+  // largest below 2^15.  With more than one block each warp makes one, and all read
+  // them from shared memory.
+  uint32_t q[kM][2];
   float2 sc[NT];    // from a score to the exponent, rows 2 t and 2 t + 1
-  int lim[NT][2];   // keys below it are visible
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    if (kMany && warp != nt) continue;
     const int row = row0 + nt * 8 + g;
     const bool in = row >= 0;
     const int tok = in ? row / G : 0;
@@ -233,16 +272,28 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        q[nt][m][i] = pack_f16x2(__uint_as_float(x[2 * m + i] << 16) * f,
+        q[m][i] = pack_f16x2(__uint_as_float(x[2 * m + i] << 16) * f,
                                  __uint_as_float(x[2 * m + i] & 0xffff0000u) * f);
+    if (kMany) {
+#pragma unroll
+      for (int m = 0; m < kM; m += 2)
+        s_q[(nt * (kM / 2) + m / 2) * 32 + lane] =
+            make_uint4(q[m][0], q[m][1], q[m + 1][0], q[m + 1][1]);
+    }
+    if (t == 0) {
+      s_back[nt * 8 + g] = back;
+      // Keys below it are visible.
+      s_lim[nt * 8 + g] = p.causal && in ? kv_len - q_len + tok + 1 : kv_len;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // A normal number: masked scores (-inf) and zeros are multiplied by it.
       (i ? sc[nt].y : sc[nt].x) =
-          fminf(fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + i) * 4) * p.scale_log2,
-                      1.17549435e-38f), 3.40282347e38f);
-      const int r = row0 + nt * 8 + 2 * t + i;
-      lim[nt][i] = p.causal && r >= 0 ? kv_len - q_len + r / G + 1 : kv_len;
+          fminf(fmaxf(s_back[nt * 8 + 2 * t + i] * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);
     }
   }
   // Steps ending at or below this key need no mask (rows are in order, so the block's
@@ -267,48 +318,58 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   bool fresh = true;  // some row has no reference yet
 
   bool failed = false;
-  int step = 0, st = 0, key0 = kv_lo + warp * C::kKeys;
+  int step = 0, st = 0, key0 = kv_lo + warp * span;
   uint32_t parity = 0;
   const int k_at = t * (D / 64);           // first group of this lane's keys
   const int v_at = D == 128 ? g : g >> 1;  // group of its values
   // One step.  kWhole: all of its keys are there and every row sees them.
   auto take = [&](auto whole, const uint8_t* stage, int left) {
     constexpr bool kWhole = decltype(whole)::value;
-#pragma unroll
+#pragma unroll(NT == 4 ? 1 : 4)
     for (int pass = 0; pass < C::kTiles; pass += C::kPass) {
       if (!kWhole && pass > 0 && pass * kFp4Tile >= left) break;
       float s[C::kPass][NT][4];
+      // (A tile behind the split's end holds what an earlier step left.)
+      // Rows of the left operand: token 2 g, and 2 g + 1 as row g + 8.
 #pragma unroll
-      for (int u = 0; u < C::kPass; ++u) {
-        // (A tile behind the split's end holds what an earlier step left.)
-        // Rows of the left operand: token 2 g, and 2 g + 1 as row g + 8.
-        const uint8_t* tile = stage + (pass + u) * F::kTileBytes;
+      for (int gg = 0; gg < D / 64; ++gg) {
+        const int j = k_at + gg;
+        uint4 k4[C::kPass];
+        uint32_t s0[C::kPass], s1[C::kPass];
 #pragma unroll
-        for (int gg = 0; gg < D / 64; ++gg) {
-          const int j = k_at + gg;
-          const uint4 k4 = *reinterpret_cast<const uint4*>(tile + F::place(j, g));
+        for (int u = 0; u < C::kPass; ++u) {
+          const uint8_t* tile = stage + (pass + u) * F::kTileBytes;
+          k4[u] = *reinterpret_cast<const uint4*>(tile + F::place(j, g));
           const uint32_t both = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(
               tile + F::kScales + j * kFp4Tile + 2 * g));
-          const uint32_t s0 = __byte_perm(both, 0, 0x1010), s1 = __byte_perm(both, 0, 0x3232);
+          s0[u] = __byte_perm(both, 0, 0x1010);
+          s1[u] = __byte_perm(both, 0, 0x3232);
+        }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < 2; ++half) {
+          const int mm = gg * 4 + half * 2;
+          uint4 qs[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            qs[nt] = kMany ? s_q[(nt * (kM / 2) + mm / 2) * 32 + lane]
+                           : make_uint4(q[mm][0], q[mm][1], q[mm + 1][0], q[mm + 1][1]);
+#pragma unroll
+          for (int u = 0; u < C::kPass; ++u) {
             uint32_t a[4], b[4];
-            fp4x8_to_f16(half ? k4.y : k4.x, a);
-            fp4x8_to_f16(half ? k4.w : k4.z, b);
+            fp4x8_to_f16(half ? k4[u].y : k4[u].x, a);
+            fp4x8_to_f16(half ? k4[u].w : k4[u].z, b);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              a[i] = mul_f16x2(a[i], s0);
-              b[i] = mul_f16x2(b[i], s1);
+              a[i] = mul_f16x2(a[i], s0[u]);
+              b[i] = mul_f16x2(b[i], s1[u]);
             }
+            const uint32_t op0[4] = {a[0], b[0], a[1], b[1]}, op1[4] = {a[2], b[2], a[3], b[3]};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t op[4] = {a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1]};
-              const int mm = gg * 4 + half * 2 + i;
+            for (int nt = 0; nt < NT; ++nt)
+              if (mm == 0) mma_16816_f16_first(s[u][nt], op0, qs[nt].x, qs[nt].y);
+              else mma_16816_f16(s[u][nt], op0, qs[nt].x, qs[nt].y);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                if (mm == 0) mma_16816_f16_first(s[u][nt], op, q[nt][mm][0], q[nt][mm][1]);
-                else mma_16816_f16(s[u][nt], op, q[nt][mm][0], q[nt][mm][1]);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma_16816_f16(s[u][nt], op1, qs[nt].z, qs[nt].w);
           }
         }
       }
@@ -321,7 +382,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
             const int key = key0 + (pass + u) * kFp4Tile + 2 * g + (x >> 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              if (key >= lim[nt][x & 1] || key >= kv_hi) s[u][nt][x] = kNegInfF;
+              if (key >= s_lim[nt * 8 + 2 * t + (x & 1)] || key >= key0 + left) s[u][nt][x] = kNegInfF;
           }
       }
       // The exponentials against the references as they are; again, against new ones,
@@ -421,7 +482,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
           wd[2][0] = hi ? v23.y : v23.x;
           wd[3][0] = hi ? v23.w : v23.z;
         }
-        if (kPairs) {
+        if (kMany) {
           const uint32_t s02 = __byte_perm(s01, s23, 0x5410), s13 = __byte_perm(s01, s23, 0x7632);
 #pragma unroll
           for (int k = 0; k < kW; ++k) {
@@ -479,10 +540,10 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     }
     copy();
     const uint8_t* stage = smem + warp * (C::kStages * C::kStage) + st * C::kStage;
-    const int left = kv_hi - key0;  // keys of the split from here on
+    const int left = min(kv_hi - key0, span);  // keys of the step
     if (key0 + C::kKeys <= free_end && left >= C::kKeys) take(std::true_type(), stage, left);
     else take(std::false_type(), stage, left);
-    key0 += kF4Warps * C::kKeys;
+    key0 += kF4Warps * span;
     st = st + 1 == C::kStages ? 0 : st + 1;
     parity ^= st == 0;
     __syncwarp();  // the stage may be filled again
@@ -502,9 +563,11 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   // Join the warps' states (their rings are done with) and write the rows.
   const int fault = __syncthreads_or((bad_page ? kErrArgF4 : 0)) ? kErrArgF4 : 0;
   const bool gone = __syncthreads_or(failed);
+  // (The kernel before this one clears the error word.)
+  if (kStatic) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) {
     const int error = gone ? kErrTimeoutF4 : fault;
-    if (PLAN) p.cta_error[blockIdx.x] = error;
+    if (kPlan) p.cta_error[blockIdx.x] = error;
     else if (error) atomicCAS(&p.hdr->error, 0, error);
   }
   float* so = reinterpret_cast<float*>(smem) + warp * kRows * D;
@@ -524,18 +587,43 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
 #pragma unroll
       for (int f = 0; f < D / 16; ++f)
         *reinterpret_cast<float2*>(so + r * D + g * (D / 8) + 2 * f) =
-            kPairs ? make_float2(o[nt][f][i], o[nt][f][i + 2])
+            kMany ? make_float2(o[nt][f][i], o[nt][f][i + 2])
                    : make_float2(o[nt][f & ~1][i + 2 * (f & 1)], o[nt][f | 1][i + 2 * (f & 1)]);
     }
   __syncthreads();
-  // Joins the warps' states: to the partial results of `to` (a slot), or to
-  // the output (to < 0), times `unit`.
+  // One row's four features from c on, joined: to the output (to < 0) or to the partial
+  // results of `to`, a slot.
+  auto put = [&](int to, int r, int c, const float4& acc, float top, float den, float unit) {
+    const float inv = den == 0.f ? 0.f : unit / den;
+    const float lse = den == 0.f ? kNegInfF : (top + __log2f(den)) * kLn2F;
+    const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (to >= 0) {
+      const size_t part = (static_cast<size_t>(to) * Hk + h) * kRows + r;
+      *reinterpret_cast<float4*>(p.o_part + part * D + c) = v;
+      if (c == 0) p.lse_part[part] = lse;
+    } else {
+      const int row = row0 + r, tok = row / G;
+      const size_t at_row = static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (row - tok * G);
+      *reinterpret_cast<uint2*>(p.out + at_row * D + c) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (c == 0 && p.lse != nullptr) p.lse[at_row] = lse;
+    }
+  };
+  // A state joins with 2^(its reference - the largest).  One without a visible key has
+  // l = 0 and O = 0 (or NaN in both, which the row then shows).
+  auto weight = [](float ref, float top) { return ref == kNegInfF ? 1.f : ex2_approx(ref - top); };
+  auto add = [](float4& acc, float f, const float4& v) {
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  };
+  // Joins this CTA's warps' states, times `unit`.
   auto join = [&](int to, float unit) {
     const float* all = reinterpret_cast<const float*>(smem);
     for (int x = threadIdx.x; x < kRows * (D / 4); x += kF4RowsThreads) {
       const int r = x / (D / 4), c = (x % (D / 4)) * 4;
-      const int row = row0 + r;
-      if (row < 0) continue;
+      if (row0 + r < 0) continue;
       float top = kNegInfF;
 #pragma unroll
       for (int v = 0; v < kF4Warps; ++v) top = fmaxf(top, s_m[v][r]);
@@ -543,36 +631,61 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int v = 0; v < kF4Warps; ++v) {
-        // A warp without a visible key has l = 0 and O = 0 (or NaN in both,
-        // which the row then shows).
-        const float f = s_m[v][r] == kNegInfF ? 1.f : ex2_approx(s_m[v][r] - top);
+        const float f = weight(s_m[v][r], top);
         den = fmaf(f, s_l[v][r], den);
-        const float4 y = *reinterpret_cast<const float4*>(all + (v * kRows + r) * D + c);
-        acc.x = fmaf(f, y.x, acc.x);
-        acc.y = fmaf(f, y.y, acc.y);
-        acc.z = fmaf(f, y.z, acc.z);
-        acc.w = fmaf(f, y.w, acc.w);
+        add(acc, f, *reinterpret_cast<const float4*>(all + (v * kRows + r) * D + c));
       }
-      const float inv = den == 0.f ? 0.f : unit / den;
-      const float ref = top == kNegInfF ? 0.f : top;
-      const float lse = den == 0.f ? kNegInfF : (ref + __log2f(den)) * kLn2F;
-      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      if (to >= 0) {
-        const size_t part = (static_cast<size_t>(to) * Hk + h) * kRows + r;
-        *reinterpret_cast<float4*>(p.o_part + part * D + c) = acc;
-        if (c == 0) p.lse_part[part] = lse;
-      } else {
-        const int tok = row / G;
-        const size_t at_row =
-            static_cast<size_t>(tok0 + tok) * p.num_heads + h * G + (row - tok * G);
-        *reinterpret_cast<uint2*>(p.out + at_row * D + c) =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-        if (c == 0 && p.lse != nullptr) p.lse[at_row] = lse;
-      }
+      put(to, r, c, acc, top, den, unit);
     }
   };
+  if (kStatic) {
+    if (fp.parts == 1) {
+      join(-1, fp.v_scale);
+    } else {
+      // Each CTA of the cluster joins its share of the rows' features over all warps of
+      // all CTAs, four lanes to four features, a warp's state of every CTA each.
+      cluster_sync();
+      const int share = (kRows * (D / 4) + fp.parts - 1) / fp.parts;
+      const int end = min(kRows * (D / 4), (rank + 1) * share);
+      const int v = threadIdx.x & 3;
+      const uint32_t at_m = smem_u32(&s_m[v][0]), at_l = smem_u32(&s_l[v][0]);
+      const uint32_t at_o = smem_u32(smem) + v * kRows * D * 4;
+      for (int x0 = rank * share; x0 < end; x0 += kF4RowsThreads / 4) {
+        const int x = x0 + (threadIdx.x >> 2);
+        const int r = min(x, end - 1) / (D / 4), c = (min(x, end - 1) % (D / 4)) * 4;
+        float ref[kF4MaxParts], top = kNegInfF;
+#pragma unroll
+        for (int i = 0; i < kF4MaxParts; ++i) {
+          ref[i] = i < fp.parts ? ld_cluster(at_m + r * 4, i) : kNegInfF;
+          top = fmaxf(top, ref[i]);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float den = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kF4MaxParts; ++i)
+          if (i < fp.parts) {
+            const float f = weight(ref[i], top);
+            den = fmaf(f, ld_cluster(at_l + r * 4, i), den);
+            add(acc, f, ld_cluster4(at_o + (r * D + c) * 4, i));
+          }
+#pragma unroll
+        for (int z = 1; z < 4; z <<= 1) {
+          den += __shfl_xor_sync(0xffffffffu, den, z);
+          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, z);
+          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, z);
+          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, z);
+          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, z);
+        }
+        if (v == 0 && x < end && row0 + r >= 0) put(-1, r, c, acc, top, den, fp.v_scale);
+      }
+      cluster_sync();  // the others have read this CTA's memory
+    }
+    return;
+  }
   join(slot, fp.v_scale);
-  if (slot < 0 || PLAN || NT > 2) return;  // else paged_merge_kernel joins them
+  if (slot < 0 || kPlan || NT > 2) return;  // else paged_merge_kernel joins them
 
   // The last of an item's splits to be done joins them all, in their order:
   // each warp takes every fourth split, with its own running maximum.
@@ -664,37 +777,56 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   join(-1, 1.f);
 }
 
-template <int D, int NT, bool PLAN>
+// Before the static kernel, which runs beside it.
+__global__ void fp4_begin_kernel(WsHeader* hdr) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  hdr->error = 0;
+  hdr->n_items = 0;
+}
+
+template <int D, int NT, Fp4Work W>
 static cudaError_t launch_fp4_rows_t(const Fp4RowsParams& p, cudaStream_t stream) {
   using C = Fp4RowsCfg<D, NT>;
-  auto kern = fp4_rows_kernel<D, NT, PLAN>;
+  auto kern = fp4_rows_kernel<D, NT, W>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.p.max_work * p.p.num_kv_heads));
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      W == Fp4Work::kStatic ? static_cast<long long>(p.p.num_seqs) * p.p.num_kv_heads * p.parts
+                            : p.p.max_work * p.p.num_kv_heads));
   cfg.blockDim = dim3(kF4RowsThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PLAN ? 0 : 1;  // after the schedule kernel
+  // After the schedule kernel, or the one above.
+  cfg.numAttrs = W == Fp4Work::kPlan ? 0 : (W == Fp4Work::kStatic && p.parts > 1 ? 2 : 1);
+  if (W == Fp4Work::kStatic) {
+    fp4_begin_kernel<<<1, 1, 0, stream>>>(p.p.hdr);
+    const cudaError_t b = cudaGetLastError();
+    if (b != cudaSuccess) return b;
+  }
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int D, int NT>
-static cudaError_t launch_fp4_rows_p(const Fp4RowsParams& p, cudaStream_t stream) {
-  return p.p.shape.plan ? launch_fp4_rows_t<D, NT, true>(p, stream)
-                        : launch_fp4_rows_t<D, NT, false>(p, stream);
+static cudaError_t launch_fp4_rows_w(const Fp4RowsParams& p, cudaStream_t stream) {
+  if (p.parts > 0) return launch_fp4_rows_t<D, NT, Fp4Work::kStatic>(p, stream);
+  return p.p.shape.plan ? launch_fp4_rows_t<D, NT, Fp4Work::kPlan>(p, stream)
+                        : launch_fp4_rows_t<D, NT, Fp4Work::kList>(p, stream);
 }
 
 template <int D>
 static cudaError_t launch_fp4_rows_d(const Fp4RowsParams& p, cudaStream_t stream) {
-  return p.p.shape.rows == 8    ? launch_fp4_rows_p<D, 1>(p, stream)
-         : p.p.shape.rows == 16 ? launch_fp4_rows_p<D, 2>(p, stream)
-                                : launch_fp4_rows_p<D, 4>(p, stream);
+  return p.p.shape.rows == 8    ? launch_fp4_rows_w<D, 1>(p, stream)
+         : p.p.shape.rows == 16 ? launch_fp4_rows_w<D, 2>(p, stream)
+                                : launch_fp4_rows_w<D, 4>(p, stream);
 }
 
 cudaError_t launch_fp4_rows(const Fp4RowsParams& p, int D, cudaStream_t stream) {

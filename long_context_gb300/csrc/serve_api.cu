@@ -186,31 +186,49 @@ bool merges(const PagedParams& p) {
   return !p.shape.join && (p.shape.plan || p.max_kv_len > p.shape.keep * p.shape.unit);
 }
 
-// Few rows over the 4-bit cache: blocks of 8, 16 or 32 rows and, above that, several of
-// 32; kFp4RowsMost rows of a KV head and more read the caches into bf16 pages first
-// and go through the tile kernel.
-constexpr int64_t kFp4RowsMost = 128;
+// Few rows over the 4-bit cache: blocks of 8, 16 or 32 rows and, above 32, three of 16
+// or two of 32; with more than kFp4RowsMost rows of a KV head the caches are read into
+// bf16 pages and go through the tile kernel.
+constexpr int64_t kFp4RowsMost = 64;
 
 PagedShape fp4_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   PagedShape s = paged_shape(group, max_seqlen, num_seqs);
   const int64_t rows = group * max_seqlen;
-  if (rows > kFp4RowsMost) return s;
+  if (rows > kFp4RowsMost) {
+    s.tiles = true;
+    return s;
+  }
   s.tiles = false;
+  s.rows = rows <= 8 ? 8 : (rows <= 16 || (rows > 32 && rows <= 48) ? 16 : 32);
   s.plan = rows <= 32 && num_seqs <= kPlanSeqs;
-  s.join = rows <= 16 && !s.plan;
-  s.rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  s.join = s.rows <= 16 && !s.plan;
   s.unit = 64;
   s.min_units = 24;
   s.whole = s.keep = 1;
-#ifndef F4_CT
-#define F4_CT 608
-#endif
-  s.ctas = F4_CT;
-#ifndef F4_C1
-#define F4_C1 3
-#endif
-  s.round = 152 * (rows <= 8 ? F4_C1 : (rows <= 16 ? 3 : 2));  // CTAs that an SM holds
+  s.ctas = 1368;
+  s.round = 152 * (s.rows <= 16 ? 3 : 2);  // CTAs that the SMs hold
   return s;
+}
+
+// CTAs to a sequence and KV head where no list is made, else 0.  As many as two thirds of
+// a round allow (a cluster's CTAs have to fit one GPC together, so a full round of them
+// does not start at once: 28 caches of 1,000 to 2,000 keys, 4 heads, 16 rows, in 448 CTAs
+// 31.5 us, by the plan 22.9).  A list makes equal splits, and costs its kernel or a join
+// behind the last split.  In several parts of up to 1,024 keys the cluster is quicker (one
+// cache of 1,000 keys, 8 heads, 11.0 and 12.3 us, of 4,000 keys 12.8 and 15.9; four of
+// 16,000, 2,000 a part, 27.6 and 27.2; eight of 3,000 to 5,000, 16 rows, 1,250 a part, 27.3
+// and 25.2), and whole caches are up to 4,096 (65 of 327 to 655 keys, 4 heads, 14.8 and
+// 19.2 us; 64 of 3,000 to 4,000, 8 heads, 66.8 and 71.3; 48 of 1,000 to 8,000, 71.1 and 66.0).
+int fp4_parts(const PagedParams& p) {
+  // One block of rows each, and few enough lengths for every CTA to check them all.
+  if (p.shape.tiles || static_cast<int64_t>(p.max_seqlen) * p.group > p.shape.rows ||
+      p.num_seqs > 1024)
+    return 0;
+  const int64_t lanes = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
+  int parts = 1;
+  while (parts < 8 && lanes * parts * 2 * 3 <= p.shape.round * 2) parts *= 2;
+  const int64_t keys = (static_cast<int64_t>(p.max_kv_len) + parts - 1) / parts;
+  return keys <= (parts > 1 ? 1024 : 4096) && lanes * parts < kInt31 ? parts : 0;
 }
 
 // The bf16 pages that the tile kernel reads: their table, keys and values.
@@ -235,7 +253,7 @@ size_t fp4_workspace(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t 
                      int32_t max_seqlen, int32_t max_kv_len) {
   const int64_t group = H / Hk;
   size_t most = 0;
-  for (const int64_t rows : {int64_t(8), int64_t(16), int64_t(32), kFp4RowsMost,
+  for (const int64_t rows : {int64_t(8), int64_t(16), int64_t(32), int64_t(48), kFp4RowsMost,
                              group * max_seqlen}) {
     const int32_t len = static_cast<int32_t>(std::min<int64_t>(max_seqlen, rows / group));
     for (const int32_t seqs : {B, std::min(B, kPlanSeqs)})
@@ -788,8 +806,9 @@ extern "C" int cpattn_paged_attn_fp4(
   p.lse = lse;
   set_workspace(p, ws, lay);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (any) f.parts = fp4_parts(p);
   // Without rows there is still the error word to write.
-  if ((!p.shape.plan || !any) && launch_paged_schedule(p, s) != cudaSuccess)
+  if (((f.parts == 0 && !p.shape.plan) || !any) && launch_paged_schedule(p, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   if (!any) return CPATTN_OK;
   if (p.shape.tiles) {
@@ -835,7 +854,7 @@ extern "C" int cpattn_paged_attn_fp4(
     f.v_scale = v_scale;
     if (launch_fp4_rows(f, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
   }
-  if (merges(p) && launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
+  if (f.parts == 0 && merges(p) && launch_paged_merge(p, head_dim, dev.num_sms, s) != cudaSuccess)
     return CPATTN_ERR_CUDA;
   return CPATTN_OK;
 }

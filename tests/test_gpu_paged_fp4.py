@@ -9,7 +9,7 @@ sum |q_i k_i| of the row; exponential, maximum and the weights of splits add 2^-
 and terms of l and O are added along chains of at most N / 32 + 700 (a warp takes two
 products a tile of 16 keys and every fourth step, a split has four warps, a merge
 joins at most 608 splits), 2^-24 each.
-With e the sum of these, numerator and denominator are both off by e.  Up to 128 rows
+With e the sum of these, numerator and denominator are both off by e.  Up to 64 rows
 of a KV head P is rounded to fp16 (2^-11 of each term, and below 2^-14, where the
 row's largest p is at least 2^11, by 2^-25: 2^-36 of the largest, N times); with more
 rows to bf16 (2^-8).  O is rounded to bf16 once (2^-8 |O|):
@@ -26,7 +26,7 @@ from test_gpu_paged import CASES
 
 pytestmark = pytest.mark.gpu
 
-MANY = 128  # rows of a KV head from which on the tile kernel works
+MANY = 64  # rows of a KV head from which on the tile kernel works
 
 
 @pytest.fixture(scope="module")
