@@ -24,9 +24,10 @@ namespace {
 
 constexpr int kF4Threads = 256;
 #ifndef F4_RUN
-#define F4_RUN 4
+#define F4_RUN 2
 #endif
-constexpr int kF4Run = F4_RUN;  // heads of a unit
+constexpr int kAppendRun = F4_RUN;  // heads of a unit of the append
+constexpr int kGatherRun = 4;  // and of the gather
 constexpr int kErrArgF = 1;  // CPATTN_ERR_INVALID_ARG
 
 // Place of a new token: its tile's first byte in head 0 of its page, or -1.
@@ -67,30 +68,39 @@ __device__ __forceinline__ uint32_t plain_zeros(uint32_t w) {
   return w & ((m + 0x77777777u) | m);  // a half's top bit survives where its m is not 0
 }
 
+// The larger magnitude of each half, of a sign that does not matter; NaN if one is.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // 16 bf16 values (two 16-byte pieces) to 8 bytes of codes and the scale byte.
 __device__ __forceinline__ uint2 quantise16(const uint4& a, const uint4& b, float inv_unit,
                                             uint32_t& scale) {
   const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  // The largest magnitude as bf16 bits: a NaN or an infinity is above every number.
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
-  top = max(top & 0xffffu, top >> 16);
-  const float t = __fdiv_rn(__uint_as_float(top << 16) * inv_unit, kFp4Top);
+  uint32_t top = max_abs2(max_abs2(max_abs2(x[0], x[1]), max_abs2(x[2], x[3])),
+                          max_abs2(max_abs2(x[4], x[5]), max_abs2(x[6], x[7])));
+  top = max(top & 0x7fffu, (top >> 16) & 0x7fffu);  // a NaN or an infinity is above the rest
+  // The quotient to 16 significant bits, which those between two scales pass exactly.
+  const float t = __uint_as_float(
+      (__float_as_uint(__uint_as_float(top << 16) * inv_unit * (1.f / kFp4Top)) + 0x80u) &
+      0xffffff00u);
   float s;
   scale = to_e4m3(fminf(fmaxf(t, kFp4MinScale), kFp4MaxScale), s);
-  const float inv = __fdiv_rn(1.f, s) * inv_unit;
+  const float inv = __fdividef(inv_unit, s);
   uint32_t code[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float q[4];
+    float2 q[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = x[2 * i + (j >> 1)];
-      const float v = __uint_as_float((j & 1) ? w & 0xffff0000u : w << 16);
-      q[j] = __fadd_rn(__fmaf_rn(v, inv, 1536.f), -1536.f);  // multiples of 2^-13
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w = x[2 * i + j];
+      q[j] = __ffma2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)),
+                        make_float2(inv, inv), make_float2(1536.f, 1536.f));
+      q[j] = __fadd2_rn(q[j], make_float2(-1536.f, -1536.f));  // multiples of 2^-13
     }
-    code[i] = to_fp4x4(q[0], q[1], q[2], q[3]);
+    code[i] = to_fp4x4(q[0].x, q[0].y, q[1].x, q[1].y);
   }
   if (top >= 0x7f80u) {
     scale = 0x7fu;
@@ -120,7 +130,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 
 }  // namespace
 
-// A group of D / 16 lanes takes kF4Run heads of a token, a lane 16 features (one
+// A group of D / 16 lanes takes kAppendRun heads of a token, a lane 16 features (one
 // scale); the groups of a warp take consecutive tokens, so that four of them fill a
 // 32-byte piece of each strip.
 template <int D>
@@ -132,11 +142,11 @@ __global__ void __launch_bounds__(kF4Threads) fp4_append_kernel(const Fp4CachePa
   const long long t = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x / LG;
   const bool live = t < p.total_tokens;
   const int token = live ? static_cast<int>(t) : 0;
-  const int h0 = static_cast<int>(blockIdx.y) * kF4Run;
-  const int heads = live ? min(h0 + kF4Run, p.kv_heads) : 0;
-  uint4 x[2][kF4Run][2];
+  const int h0 = static_cast<int>(blockIdx.y) * kAppendRun;
+  const int heads = live ? min(h0 + kAppendRun, p.kv_heads) : 0;
+  uint4 x[2][kAppendRun][2];
 #pragma unroll
-  for (int i = 0; i < kF4Run; ++i)
+  for (int i = 0; i < kAppendRun; ++i)
 #pragma unroll
     for (int w = 0; w < 2; ++w)
       if (h0 + i < heads) {
@@ -155,7 +165,7 @@ __global__ void __launch_bounds__(kF4Threads) fp4_append_kernel(const Fp4CachePa
   for (int w = 0; w < 2; ++w) {
     uint8_t* cache = (w ? p.v_cache : p.k_cache) + at.at;
 #pragma unroll
-    for (int i = 0; i < kF4Run; ++i) {
+    for (int i = 0; i < kAppendRun; ++i) {
       if (h0 + i >= heads) break;
       uint32_t scale;
       const uint2 code = quantise16(x[w][i][0], x[w][i][1], w ? p.v_scale : p.k_scale, scale);
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(kF4Threads) fp4_append_kernel(const Fp4CachePa
   }
 }
 
-// D / 8 lanes write a row, 16 bytes each; they take kF4Run heads of a token, and a
+// D / 8 lanes write a row, 16 bytes each; they take kGatherRun heads of a token, and a
 // CTA consecutive tokens, whose codes lie in the same 32-byte pieces.
 template <int D>
 __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CacheParams p) {
@@ -177,8 +187,8 @@ __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CachePa
   const long long t = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x / LG;
   const bool live = t < p.total_tokens;
   const int token = live ? static_cast<int>(t) : 0;
-  const int h0 = static_cast<int>(blockIdx.y) * kF4Run;
-  const int heads = min(h0 + kF4Run, p.kv_heads);
+  const int h0 = static_cast<int>(blockIdx.y) * kGatherRun;
+  const int heads = min(h0 + kGatherRun, p.kv_heads);
   const Fp4Place at = find_place<LG>(p, Fp4<D>::kTileBytes, live, token, c, lane);
   if (at.at < 0) {
     if (live && !at.behind && p.status != nullptr && c == 0) atomicCAS(p.status, 0, kErrArgF);
@@ -187,9 +197,9 @@ __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CachePa
   const long long block = (1ll << p.page_shift) / kFp4Tile * Fp4<D>::kTileBytes;
   const int code_at = Fp4<D>::place(j, at.row >> 1) + (at.row & 1) * 8 + (c & 1) * 4;
   const int scale_at = Fp4<D>::kScales + j * kFp4Tile + at.row;
-  uint32_t code[2][kF4Run], scale[2][kF4Run];
+  uint32_t code[2][kGatherRun], scale[2][kGatherRun];
 #pragma unroll
-  for (int i = 0; i < kF4Run; ++i)
+  for (int i = 0; i < kGatherRun; ++i)
 #pragma unroll
     for (int w = 0; w < 2; ++w)
       if (h0 + i < heads) {
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CachePa
     __nv_bfloat16* out =
         w ? p.v_out + token * p.v_stride : p.k_out + token * p.k_stride;
 #pragma unroll
-    for (int i = 0; i < kF4Run; ++i)
+    for (int i = 0; i < kGatherRun; ++i)
       if (h0 + i < heads)
         *reinterpret_cast<uint4*>(out + (h0 + i) * D + c * 8) =
             values8(code[w][i], e4m3_value(scale[w][i]) * (w ? p.v_scale : p.k_scale));
@@ -264,21 +274,23 @@ __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesPar
   if (bad && lane == 0) atomicCAS(&p.hdr->error, 0, kErrArgF);
 }
 
-static dim3 fp4_grid(const Fp4CacheParams& p, int lanes) {
+static dim3 fp4_grid(const Fp4CacheParams& p, int lanes, int run) {
   const long long tokens = kF4Threads / lanes;
   return dim3(static_cast<unsigned>((p.total_tokens + tokens - 1) / tokens),
-              static_cast<unsigned>((p.kv_heads + kF4Run - 1) / kF4Run));
+              static_cast<unsigned>((p.kv_heads + run - 1) / run));
 }
 
 cudaError_t launch_fp4_append(const Fp4CacheParams& p, int D, cudaStream_t stream) {
-  if (D == 64) fp4_append_kernel<64><<<fp4_grid(p, 4), kF4Threads, 0, stream>>>(p);
-  else fp4_append_kernel<128><<<fp4_grid(p, 8), kF4Threads, 0, stream>>>(p);
+  const dim3 grid = fp4_grid(p, D / 16, kAppendRun);
+  if (D == 64) fp4_append_kernel<64><<<grid, kF4Threads, 0, stream>>>(p);
+  else fp4_append_kernel<128><<<grid, kF4Threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_fp4_gather(const Fp4CacheParams& p, int D, cudaStream_t stream) {
-  if (D == 64) fp4_gather_kernel<64><<<fp4_grid(p, 8), kF4Threads, 0, stream>>>(p);
-  else fp4_gather_kernel<128><<<fp4_grid(p, 16), kF4Threads, 0, stream>>>(p);
+  const dim3 grid = fp4_grid(p, D / 8, kGatherRun);
+  if (D == 64) fp4_gather_kernel<64><<<grid, kF4Threads, 0, stream>>>(p);
+  else fp4_gather_kernel<128><<<grid, kF4Threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
