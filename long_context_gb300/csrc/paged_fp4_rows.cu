@@ -75,6 +75,11 @@ struct Fp4RowsCfg {
   static constexpr int kCtas = NT == 4 ? 2 : 3;  // of an SM
 };
 
+// The low halves of lo's bytes and the high halves of hi's.
+__device__ __forceinline__ uint32_t halves(uint32_t lo, uint32_t hi) {
+  return (lo & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);
+}
+
 __device__ __forceinline__ void sts128_zero(uint32_t a) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
 }
@@ -462,7 +467,8 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
           const int n = kv_len - (key0 + (pass + u) * kFp4Tile) - 4 * t;
           sb = n <= 0 ? 0u : (n >= 4 ? sb : sb & ((1u << (8 * n)) - 1u));
         }
-        const uint32_t s01 = e4m3x2_to_f16(sb), s23 = e4m3x2_to_f16(sb >> 16);
+        sb = __byte_perm(sb, 0, 0x3120);
+        const uint32_t s02 = e4m3x2_to_f16(sb), s13 = e4m3x2_to_f16(sb >> 16);
         // Words of the four tokens, eight features each.
         constexpr int kW = D / 64;
         uint32_t wd[4][kW];
@@ -482,49 +488,20 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
           wd[2][0] = hi ? v23.y : v23.x;
           wd[3][0] = hi ? v23.w : v23.z;
         }
-        if (kMany) {
-          const uint32_t s02 = __byte_perm(s01, s23, 0x5410), s13 = __byte_perm(s01, s23, 0x7632);
 #pragma unroll
-          for (int k = 0; k < kW; ++k) {
-            uint32_t x[4][4];
+        for (int k = 0; k < kW; ++k) {
+          uint32_t x[2][2][4];  // tokens (0, 2) or (1, 3), even or odd feature
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fp4x8_to_f16(wd[i][k], x[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t op[4] = {
-                  mul_f16x2(__byte_perm(x[0][i], x[2][i], 0x5410), s02),
-                  mul_f16x2(__byte_perm(x[0][i], x[2][i], 0x7632), s02),
-                  mul_f16x2(__byte_perm(x[1][i], x[3][i], 0x5410), s13),
-                  mul_f16x2(__byte_perm(x[1][i], x[3][i], 0x7632), s13)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_16816_f16(o[nt][k * 4 + i], op, pa[nt], pb[nt]);
-            }
+          for (int z = 0; z < 2; ++z) {
+            fp4x8_to_f16(halves(wd[z][k], wd[z + 2][k] << 4), x[z][0]);
+            fp4x8_to_f16(halves(wd[z][k] >> 4, wd[z + 2][k]), x[z][1]);
           }
-        } else {
-          const uint32_t sx[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                                  __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-          // P with the other feature's column zero, tokens (0, 2) and (1, 3).
-          const uint32_t lo[2][2] = {{pa[0] & 0xffffu, pa[0] >> 16}, {pb[0] & 0xffffu, pb[0] >> 16}};
-          const uint32_t hi[2][2] = {{pa[0] << 16, pa[0] & 0xffff0000u},
-                                     {pb[0] << 16, pb[0] & 0xffff0000u}};
 #pragma unroll
-          for (int k = 0; k < kW; ++k) {
-            uint32_t x[4][4];
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t op[4] = {mul_f16x2(x[0][0][i], s02), mul_f16x2(x[0][1][i], s02),
+                                    mul_f16x2(x[1][0][i], s13), mul_f16x2(x[1][1][i], s13)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              fp4x8_to_f16(wd[i][k], x[i]);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) x[i][y] = mul_f16x2(x[i][y], sx[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; i += 2)
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const uint32_t op[4] = {x[z][i], x[z][i + 1], x[z + 2][i], x[z + 2][i + 1]};
-                mma_16816_f16(o[0][k * 4 + i], op, lo[z][0], lo[z][1]);
-                mma_16816_f16(o[0][k * 4 + i + 1], op, hi[z][0], hi[z][1]);
-              }
+            for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][k * 4 + i], op, pa[nt], pb[nt]);
           }
         }
       }
@@ -587,8 +564,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
 #pragma unroll
       for (int f = 0; f < D / 16; ++f)
         *reinterpret_cast<float2*>(so + r * D + g * (D / 8) + 2 * f) =
-            kMany ? make_float2(o[nt][f][i], o[nt][f][i + 2])
-                   : make_float2(o[nt][f & ~1][i + 2 * (f & 1)], o[nt][f | 1][i + 2 * (f & 1)]);
+            make_float2(o[nt][f][i], o[nt][f][i + 2]);
     }
   __syncthreads();
   // One row's four features from c on, joined: to the output (to < 0) or to the partial
