@@ -591,7 +591,7 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  * Pages, page_table, kv_lens and cu_seqlens are those of the bf16 cache above, but
  * k_cache and v_cache are bytes [num_pages, num_kv_heads, page_size * 9 D / 16],
  * 16-byte aligned, a page contiguous and page_stride BYTES from page to page (a
- * multiple of 16).  A page of one head is page_size / 16 tiles of 9 D bytes, tile i
+ * multiple of 16, below 2^36).  A page of one head is page_size / 16 tiles of 9 D bytes, tile i
  * for its tokens 16 i .. 16 i + 15.  In a tile:
  *   for each group j of 16 features a strip of 128 bytes at 128 j: token r of the
  *   tile has its 8 bytes at 16 ((r / 2) ^ (128 j / D)) + 8 (r % 2), features 16 j +

@@ -370,11 +370,11 @@ struct Fp4PagesParams {
 // Follows the schedule kernel (as its programmatic dependent).
 cudaError_t launch_fp4_pages(const Fp4PagesParams& p, int D, cudaStream_t stream);
 
-// Few rows: PagedParams with the caches' addresses and strides in bytes.
+// Few rows: PagedParams with the 4-bit caches.
 struct Fp4RowsParams {
   PagedParams p;
   const uint8_t *k_cache, *v_cache;
-  long long page_stride;
+  uint32_t page_units;               // page stride in units of 16 bytes
   float v_scale;                     // (p.scale_log2 has the keys')
   int parts;                         // > 0: so many CTAs to a sequence and KV head, no list
 };

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   int copy_key = kv_lo + warp * span + run_at * kFp4Tile;  // of the next copy
   uint32_t copy_to = ring + (lane & 1) * C::kHalf + run_at * F::kTileBytes;
   uint32_t copy_bar = smem_u32(full);
+  const uint32_t page_units = fp.page_units;
   int copy_left = steps;
   int next_page = copy_key < copy_end ? __ldg(pages + (copy_key >> p.page_shift)) : 0;
   bool bad_page = false;
@@ -215,11 +216,13 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     if (key < copy_end) {
       const int n = min(run_tiles, (copy_end - key + kFp4Tile - 1) / kFp4Tile);
       if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
-        const int at = (key >> 4) & (page_tiles - 1);
+        const unsigned at = (key >> 4) & (page_tiles - 1);
         const uint32_t bytes = n * F::kTileBytes;
         mbar_expect_tx(copy_bar, bytes);
         if (!drop)
-          bulk_load(copy_to, cache + static_cast<size_t>(page) * fp.page_stride + at * F::kTileBytes,
+          bulk_load(copy_to,
+                    cache + (static_cast<uint64_t>(static_cast<unsigned>(page)) * page_units +
+                             at * (F::kTileBytes / 16)) * 16,
                     bytes, copy_bar);
       } else {
         // Its keys or values count as zeros: their scales are.

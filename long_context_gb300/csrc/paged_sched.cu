@@ -534,10 +534,11 @@ __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(const PagedPara
     int error = 0;
     for (int i = threadIdx.x; i < plan.splits * p.num_kv_heads; i += kPmThreads)
       error |= __ldcg(p.cta_error + i);
-    error = __syncthreads_or(error);
+    const bool bad = __syncthreads_or(plan.bad || (error & 1));
+    const bool late = __syncthreads_or(error & 6);
     if (threadIdx.x == 0) {
-      // CPATTN_ERR_INVALID_ARG, or a wait's CPATTN_ERR_DEVICE_TIMEOUT.
-      p.hdr->error = plan.bad || (error & 1) ? 1 : error;
+      // CPATTN_ERR_INVALID_ARG, CPATTN_ERR_DEVICE_TIMEOUT
+      p.hdr->error = bad ? 1 : (late ? 6 : 0);
       p.hdr->n_items = plan.splits;
       p.hdr->pad[0] = plan.merges;
     }

@@ -281,7 +281,8 @@ int check_fp4(int64_t num_pages, int32_t page_size, int64_t page_stride, int32_t
   if (D != 64 && D != 128) return CPATTN_ERR_UNSUPPORTED;
   if (page_shift_of(page_size) < 0) return CPATTN_ERR_UNSUPPORTED;
   if (Hk < 1 || Hk > 65535 || num_pages < 1 || num_pages >= kInt31 || max_pages < 0 ||
-      page_stride < static_cast<int64_t>(page_size) * Hk * 9 * D / 16 || page_stride % 16 != 0)
+      page_stride < static_cast<int64_t>(page_size) * Hk * 9 * D / 16 || page_stride % 16 != 0 ||
+      page_stride / 16 >= int64_t(1) << 32)
     return CPATTN_ERR_INVALID_ARG;
   if (!unit_ok(k_scale) || !unit_ok(v_scale)) return CPATTN_ERR_INVALID_ARG;
   return CPATTN_OK;
@@ -850,7 +851,7 @@ extern "C" int cpattn_paged_attn_fp4(
   } else {
     f.k_cache = static_cast<const uint8_t*>(k_cache);
     f.v_cache = static_cast<const uint8_t*>(v_cache);
-    f.page_stride = page_stride;
+    f.page_units = static_cast<uint32_t>(page_stride / 16);
     f.v_scale = v_scale;
     if (launch_fp4_rows(f, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
   }
