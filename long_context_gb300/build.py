@@ -104,7 +104,7 @@ def build_debug(force=False):
     and TMA coordinate they derive and report a violation as
     CPATTN_ERR_DEVICE_BOUNDS in the workspace error word (never a trap).
     Same C ABI as libcpattn.so.  The norm + rotation and paged-cache kernels have no
-    such checks, and the binding's four calls of them (``_binding.so`` is linked to
+    such checks, and the binding's calls of them (``_binding.so`` is linked to
     libcpattn.so) do not reach this library when ``cpattn._lib`` is swapped for it."""
     return _build_variant("cpattn_debug", "CPATTN_DEBUG", force)
 

@@ -368,7 +368,7 @@ struct Fp4PagesParams {
 };
 
 // Follows the schedule kernel (as its programmatic dependent).
-cudaError_t launch_fp4_pages(const Fp4PagesParams& p, int D, cudaStream_t stream);
+cudaError_t launch_fp4_pages(const Fp4PagesParams& p, int D, int num_sms, cudaStream_t stream);
 
 // Few rows: PagedParams with the 4-bit caches.
 struct Fp4RowsParams {

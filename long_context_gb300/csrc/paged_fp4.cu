@@ -6,11 +6,15 @@
 // both to the nearest, halves to even, c saturating.  x has 8 significant bits and s
 // four, so a border between two codes times s has at most 7: x is either on a border
 // or off it by 2^-8 of it, and x times the rounded reciprocal of s, rounded to
-// multiples of 2^-13, falls on the same side as the quotient.  The bytes are those
-// that exact arithmetic gives.  A group with a NaN or an infinity gets the scale NaN.
+// multiples of 2^-13, falls on the same side as the quotient (for s: 16
+// significant bits).  The bytes are those that exact arithmetic gives.  A group with a
+// NaN or an infinity gets the scale NaN.
 //
-// All three are HBM bound: 2.56 bytes a feature, and fewer than 6 instructions where
-// the bytes take the time of 14.
+// All three are HBM bound, 2.56 bytes a feature; the append spends 7 instructions on one
+// where its bytes take the time of 14.  A lane takes 16 features of the append, one scale,
+// and 8 of the others, 16 bytes of bf16.  60,000 tokens of 8 heads of 128 take 49.4 us in
+// (6.4 TB/s with 4 us for the launch) and 51.5 us out; 16 caches of 300,000 tokens in all
+// 304 us (6.4 TB/s); 34,816 tokens into pages 28 us (6.5 TB/s).
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -23,11 +27,10 @@ namespace cpattn {
 namespace {
 
 constexpr int kF4Threads = 256;
-#ifndef F4_RUN
-#define F4_RUN 2
-#endif
-constexpr int kAppendRun = F4_RUN;  // heads of a unit of the append
-constexpr int kGatherRun = 4;  // and of the gather
+constexpr int kAppendRun = 2;  // heads of a unit of the append (of four: 47 registers more,
+                               // a decoding step's pass 11.7 instead of 10.1 us)
+constexpr int kGatherRun = 4;  // and of the gather (of two: 16 caches 324 instead of 304 us)
+constexpr int kPagesCtas = 8;  // CTAs of an SM, the pages' kernel
 constexpr int kErrArgF = 1;  // CPATTN_ERR_INVALID_ARG
 
 // Place of a new token: its tile's first byte in head 0 of its page, or -1.
@@ -220,9 +223,10 @@ __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CachePa
 }
 
 // Caches [0, kv_len) of every sequence to bf16 pages of 128 tokens, page i of
-// sequence b at b * out_pages + i, with the table that says so.  A CTA has one such
-// page and KV head, a warp a tile of it.  Keys are left without the cache's power of
-// two (it is in the softmax scale), values get it, exactly.
+// sequence b at b * out_pages + i, with the table that says so.  A CTA has a KV head and
+// every gridDim.x-th of the pages that there are (the bounds may be far above the
+// lengths), a warp a tile of it.  Keys are left without the cache's power of two (it is
+// in the softmax scale), values get it, exactly.
 template <int D>
 __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesParams p) {
   constexpr int LG = D / 8;
@@ -230,44 +234,55 @@ __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesPar
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane % LG, j = c >> 1;
-  const long long to = blockIdx.x;
-  const int h = static_cast<int>(blockIdx.y);
-  const int b = static_cast<int>(static_cast<unsigned>(to) / p.out_pages);
-  const int pg = static_cast<int>(to - static_cast<long long>(b) * p.out_pages);
-  const int kv = __ldg(p.kv_lens + b);
+  const int h = static_cast<int>(blockIdx.y), step = static_cast<int>(gridDim.x);
   const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
-  const int key0 = pg * kFp4OutPage + warp * kFp4Tile;
-  if (h == 0 && threadIdx.x == 0) p.out_table[to] = static_cast<int>(to);
+  const long long block = (1ll << p.page_shift) / kFp4Tile * Fp4<D>::kTileBytes;
   bool bad = false;
-  if (kv >= 0 && kv <= p.max_kv_len && kv <= cap && key0 < kv) {
-    int page = __ldg(p.page_table + static_cast<size_t>(b) * p.max_pages + (key0 >> p.page_shift));
-    bad = page < 0 || page >= p.num_pages;
-    const long long block = (1ll << p.page_shift) / kFp4Tile * Fp4<D>::kTileBytes;
-    const long long at = static_cast<long long>(bad ? 0 : page) * p.page_stride + h * block +
-                         ((key0 & ((1 << p.page_shift) - 1)) / kFp4Tile) * Fp4<D>::kTileBytes;
-    const int n = min(kv - key0, kFp4Tile);
+  int first = static_cast<int>(blockIdx.x);  // of this CTA's pages of sequence b
+  int kv_next = p.num_seqs > 0 ? __ldg(p.kv_lens) : 0;
+  for (int b = 0; b < p.num_seqs; ++b) {
+    const int kv = kv_next;
+    if (b + 1 < p.num_seqs) kv_next = __ldg(p.kv_lens + b + 1);
+    // (The schedule kernel reports lengths that are not valid.)
+    const bool valid = kv >= 0 && kv <= p.max_kv_len && kv <= cap;
+    const int n_pages = valid ? (kv + kFp4OutPage - 1) / kFp4OutPage : 0;
+    const int* pages = p.page_table + static_cast<size_t>(b) * p.max_pages;
+    int pg = first;
+    for (; pg < n_pages; pg += step) {
+      const long long to = static_cast<long long>(b) * p.out_pages + pg;
+      if (h == 0 && threadIdx.x == 0) p.out_table[to] = static_cast<int>(to);
+      const int key0 = pg * kFp4OutPage + warp * kFp4Tile;
+      if (key0 >= kv) continue;
+      const int page = __ldg(pages + (key0 >> p.page_shift));
+      const bool gone = page < 0 || page >= p.num_pages;
+      bad = bad || gone;
+      const long long at = static_cast<long long>(gone ? 0 : page) * p.page_stride + h * block +
+                           ((key0 & ((1 << p.page_shift) - 1)) / kFp4Tile) * Fp4<D>::kTileBytes;
+      const int n = min(kv - key0, kFp4Tile);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint8_t* tile = (w ? p.v_cache : p.k_cache) + at;
-      __nv_bfloat16* out = (w ? p.v_out : p.k_out) +
-                           ((to * kFp4OutPage + warp * kFp4Tile) * p.kv_heads + h) * D + c * 8;
-      uint32_t code[kFp4Tile / kRows], scale[kFp4Tile / kRows];
+      for (int w = 0; w < 2; ++w) {
+        const uint8_t* tile = (w ? p.v_cache : p.k_cache) + at;
+        __nv_bfloat16* out = (w ? p.v_out : p.k_out) +
+                             ((to * kFp4OutPage + warp * kFp4Tile) * p.kv_heads + h) * D + c * 8;
+        uint32_t code[kFp4Tile / kRows], scale[kFp4Tile / kRows];
 #pragma unroll
-      for (int i = 0; i < kFp4Tile / kRows; ++i) {
-        const int r = i * kRows + lane / LG;
-        code[i] = __ldg(reinterpret_cast<const uint32_t*>(
-            tile + Fp4<D>::place(j, r >> 1) + (r & 1) * 8 + (c & 1) * 4));
-        scale[i] = __ldg(tile + Fp4<D>::kScales + j * kFp4Tile + r);
-      }
+        for (int i = 0; i < kFp4Tile / kRows; ++i) {
+          const int r = i * kRows + lane / LG;
+          code[i] = __ldg(reinterpret_cast<const uint32_t*>(
+              tile + Fp4<D>::place(j, r >> 1) + (r & 1) * 8 + (c & 1) * 4));
+          scale[i] = __ldg(tile + Fp4<D>::kScales + j * kFp4Tile + r);
+        }
 #pragma unroll
-      for (int i = 0; i < kFp4Tile / kRows; ++i) {
-        const int r = i * kRows + lane / LG;
-        const float s = e4m3_value(scale[i]) * (w ? p.v_scale : 1.f);
-        if (r < n)
-          *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * p.kv_heads * D) =
-              bad ? make_uint4(0u, 0u, 0u, 0u) : values8(code[i], s);
+        for (int i = 0; i < kFp4Tile / kRows; ++i) {
+          const int r = i * kRows + lane / LG;
+          const float s = e4m3_value(scale[i]) * (w ? p.v_scale : 1.f);
+          if (r < n)
+            *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * p.kv_heads * D) =
+                gone ? make_uint4(0u, 0u, 0u, 0u) : values8(code[i], s);
+        }
       }
     }
+    first = pg - n_pages;  // the pages of all sequences are dealt out in turn
   }
   // The schedule before this clears the error word.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -294,9 +309,12 @@ cudaError_t launch_fp4_gather(const Fp4CacheParams& p, int D, cudaStream_t strea
   return cudaGetLastError();
 }
 
-cudaError_t launch_fp4_pages(const Fp4PagesParams& p, int D, cudaStream_t stream) {
+cudaError_t launch_fp4_pages(const Fp4PagesParams& p, int D, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.num_seqs) * p.out_pages),
+  // Two rounds of CTAs over all heads, and no more than there can be pages.
+  const long long pages = static_cast<long long>(p.num_seqs) * p.out_pages;
+  const long long share = (num_sms * kPagesCtas + p.kv_heads - 1) / p.kv_heads;
+  cfg.gridDim = dim3(static_cast<unsigned>(pages < share ? pages : share),
                      static_cast<unsigned>(p.kv_heads));
   cfg.blockDim = dim3(kF4Threads);
   cfg.stream = stream;

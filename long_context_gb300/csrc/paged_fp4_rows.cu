@@ -1,33 +1,47 @@
 // Attention of few rows over a paged KV cache in 4 bits (fp4.cuh): one token a
 // sequence, or a few, for every query head that shares a KV head.
 //
-// The work is cut as for the bf16 cache (paged_rows.cu): a CTA of 4 warps has one
-// block of 8, 16 or 32 rows of one KV head and one split of the keys, and each warp
-// takes every fourth step of the split on its own, with its own ring of stages, its
-// own softmax state and no barrier until the states are joined.  What differs is what
-// bounds it: a key and its value are 9 D / 8 bytes instead of 4 D, so at the copy
-// bandwidth an SM has 98 cycles for a tile of 16 keys of 128 features and their
-// values, in which 4,096 codes become fp16 operands.  (Measured rates of an SM: 43
-// conversions of two codes a cycle with the byte taken out of its word, 64 packed
-// multiplications, 64 permutations, 0.57 matrix instructions.)  So:
+// A CTA of 4 warps has one block of 8, 16 or 32 rows of one KV head and one split of the
+// keys, and each warp takes every fourth step of the split on its own, with its own
+// ring of stages, its own softmax state and no barrier until the states are joined
+// (as for the bf16 cache, paged_rows.cu).  What differs is what bounds it: a key and its
+// value are 9 D / 8 bytes instead of 4 D, so at the copy bandwidth an SM has 98 cycles
+// for a tile of 16 keys of 128 features and their values, in which 4,096 codes become
+// fp16 operands.  Measured rates of an SM, a cycle: 64 conversions of two codes, as many packed
+// multiplications, permutations or logic operations, and 0.57 matrix instructions.  So:
 // * keys and values are the left operand of 16 x 8 x 16 matrix instructions, whose
 //   16 rows they fill, and the queries are the right one: 8 rows cost 8 instructions
 //   for a tile's scores, not 16;
 // * scores come out as [keys, rows]; the matrix transpose that P needs between the
 //   products is one instruction for 8 x 8;
-// * a code pair (features 2 i and 2 i + 1 of one key) is a pair of fp16 as it comes
-//   out of the conversion.  Keys take it as it is.  The values' operand has pairs of
-//   keys: with one block of 8 rows, the pair is used as two columns of the operand
-//   instead, and P's column for the other feature is zero, so each feature of a pair
-//   costs a product (8 more instructions a tile instead of 32 permutations a lane);
-//   with more rows the pairs are permuted;
+// * a byte of codes (features 2 i and 2 i + 1 of one key) is a pair of fp16 as it comes
+//   out of one conversion, and keys take it as it is.  The values' operand has pairs of
+//   keys: the halves of two keys' words are exchanged before the conversion, 16
+//   operations a tile and lane (permutations behind it, 32; without them, the other
+//   feature's column of P zero and twice the products: a token each of 64 caches, 32 / 8
+//   heads of 128, 247 instead of 238 us);
 // * codes times scales are exact in fp16, the queries (each row times a power of two,
-//   which the score's factor takes back) too; P is rounded to fp16 (2^-12);
-// * K and V come by bulk copies, one a page and operand, a few lanes issuing them.
+//   which the score's factor takes back) too; P is rounded to fp16 (2^-11);
+// * K and V come by bulk copies, one a page and operand, a few lanes issuing them;
+// * a step is 64 keys of 128 features and its scores are taken together: with 32 at a
+//   time, and four CTAs of an SM instead of three, 277 instead of 247 us.
+// That case is at 5.9 TB/s (1.40 GB in 238 us; the same copies without the arithmetic
+// take 214): 242 instructions a tile and warp at half of the issue rate, by latencies of
+// the chain copy, conversion, scores, exponentials, P V in 12 warps of 150 registers.
+// With 32 rows the products are four times as many (17 caches of up to 20,000 keys, 4
+// KV heads of 64, 25 rows: 40 us, of which 31 are left without the products); their
+// queries are in shared memory (in registers, which spilled, 72 instead of 62 us for
+// 32 rows over 17 caches of 128 features).
 //
-// Softmax: p = 2^(s scale log2 e - m + 11), a running reference m per row that moves
-// when a score exceeds it by 4 powers of two; p is then below 2^15 and keeps fp16's
-// 11 bits down to 2^-25 of the largest weight.  l sums p in fp32.
+// Softmax: p = 2^(s scale log2 e - m + 11) with a running reference m per row.  It is
+// the largest score of the first keys and moves to a new largest only when a lane's sum
+// of a pass would leave fp16's range, so p is below 2^15 and the largest weight's at
+// least 2^11: fp16 keeps its 11 bits of weights down to 2^-25 of the largest.  O and l
+// share the reference, so O / l and m + ln l do not depend on it.  l sums p in fp32.
+//
+// The splits come from the schedule kernel's list, from the lengths in every warp
+// (paged_plan.cuh), or, where sequences are short, are equal parts of a sequence that a
+// cluster of CTAs takes, whose states meet through distributed shared memory.
 #include <cuda_bf16.h>
 
 #include <type_traits>

@@ -187,8 +187,13 @@ bool merges(const PagedParams& p) {
 }
 
 // Few rows over the 4-bit cache: blocks of 8, 16 or 32 rows and, above 32, three of 16
-// or two of 32; with more than kFp4RowsMost rows of a KV head the caches are read into
-// bf16 pages and go through the tile kernel.
+// (40 rows over 20 caches of 5,000 to 15,000 keys, 4 heads of 128: 115 us, in two blocks
+// of 32 rows 124) or two of 32 (64 rows of 64: 82 and 89); with more than kFp4RowsMost
+// rows of a KV head the caches are read into bf16 pages and go through the tile kernel
+// (72 rows, the same caches: 170 by blocks and 177; 125 rows over nine caches 181 and 118;
+// 64 rows of 64 82 and 107).  Splits of less than 24 units cost more in joins than they
+// even out, and of more than 1 / 1368 of all work leave the SMs uneven (a token each of 64
+// caches: 608 splits aimed at 277 us, 1368 247, 2736 246).
 constexpr int64_t kFp4RowsMost = 64;
 
 PagedShape fp4_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
@@ -832,7 +837,7 @@ extern "C" int cpattn_paged_attn_fp4(
     g.page_stride = page_stride;
     g.v_scale = v_scale;
     g.hdr = p.hdr;
-    if (pages.pages > 0 && launch_fp4_pages(g, head_dim, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+    if (pages.pages > 0 && launch_fp4_pages(g, head_dim, dev.num_sms, s) != cudaSuccess) return CPATTN_ERR_CUDA;
     p.k_cache = g.k_out;
     p.v_cache = g.v_out;
     p.page_table = g.out_table;

@@ -610,3 +610,34 @@ def test_refused_tensors(cp):
         cp.alloc_fp4_cache(4, 16, 2, 96)
     out, lse = cp.paged_attn_fp4(**good, **bounds)
     x.check(out, lse)
+
+
+@pytest.mark.parametrize("bound", [1, 5, 12, 40])
+def test_bounds_far_above_the_lengths(cp, bound):
+    """A captured program's bounds: a million keys, more sequences than have keys."""
+    x = Batch4([1, 0, 1, 1], [300, 0, 7, 129], 8, 2, 64, 32, seed=33)
+    ws = cp.alloc_paged_fp4_workspace(x.T, 4, 8, 2, 64, bound, 1 << 20)
+    out, lse = cp.paged_attn_fp4(*x.on_gpu(), max_seqlen=bound, max_kv_len=1 << 20, workspace=ws)
+    assert cp.poll_error(ws) == cp.OK
+    x.check(out, lse, bound=bound)
+
+
+def test_two_calls_and_two_workspaces_at_once(cp):
+    """Two streams, each with its own workspace, in every form of the work list."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for new, kv, bound in (([1, 1], [900, 70], 900), ([1, 1], [900, 70], 30000),
+                           ([4, 3], [900, 70], 30000), ([1] * 40, [60 + b for b in range(40)], 99),
+                           ([1] * 40, [60 + b for b in range(40)], 30000), ([30, 40], [900, 70], 900)):
+        xs = [Batch4(new, kv, 10, 2, 128, 16, seed=41 + i) for i in range(2)]
+        args = [x.on_gpu() for x in xs]
+        ws = [cp.alloc_paged_fp4_workspace(x.T, len(kv), 10, 2, 128, max(new), bound) for x in xs]
+        torch.cuda.synchronize()
+        outs = [None, None]
+        for _ in range(3):
+            for i in range(2):
+                outs[i] = cp.paged_attn_fp4(*args[i], max_seqlen=max(new), max_kv_len=bound,
+                                            workspace=ws[i], stream=streams[i])
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert cp.poll_error(ws[i]) == cp.OK
+            xs[i].check(*outs[i])
