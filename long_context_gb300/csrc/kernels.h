@@ -291,6 +291,7 @@ struct PagedShape {
   int round;       // CTAs resident at once (at most ctas)
   bool join;       // the last CTA of a split item joins it (else a merge kernel)
   bool plan;       // no schedule kernel: every warp works the list out (paged_plan.cuh)
+  bool fit;        // its splits as small as one round's slots allow
 };
 
 struct PagedParams {

@@ -29,9 +29,9 @@
 // take 214): 242 instructions a tile and warp at half of the issue rate, by latencies of
 // the chain copy, conversion, scores, exponentials, P V in 12 warps of 150 registers.
 // With 32 rows the products are four times as many (17 caches of up to 20,000 keys, 4
-// KV heads of 64, 25 rows: 40 us, of which 31 are left without the products); their
+// KV heads of 64, 25 rows: 37 us, 9 of them the products' and their operands'); their
 // queries are in shared memory (in registers, which spilled, 72 instead of 62 us for
-// 32 rows over 17 caches of 128 features).
+// 32 rows over 17 caches of 128 features, now 56).
 //
 // Softmax: p = 2^(s scale log2 e - m + 11) with a running reference m per row.  It is
 // the largest score of the first keys and moves to a new largest only when a lane's sum

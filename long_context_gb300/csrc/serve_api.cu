@@ -64,6 +64,7 @@ int page_shift_of(int32_t page_size) {
 PagedShape paged_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   PagedShape s;
   const int64_t rows = group * max_seqlen;
+  s.fit = false;
   s.tiles = rows > 32;
   // A sequence's rows are one block, a lane's to plan.
   s.plan = !s.tiles && num_seqs <= kPlanSeqs;
@@ -212,6 +213,7 @@ PagedShape fp4_shape(int64_t group, int32_t max_seqlen, int32_t num_seqs) {
   s.whole = s.keep = 1;
   s.ctas = 1368;
   s.round = 152 * (s.rows <= 16 ? 3 : 2);  // CTAs that the SMs hold
+  s.fit = true;
   return s;
 }
 
