@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   __shared__ float s_back[kRows];
   __shared__ int s_lim[kRows];
   __shared__ uint4 s_q[kMany ? NT * (kM / 2) * 32 : 1];
-  __shared__ int s_last, s_abort;
+  __shared__ int s_last, s_abort, s_bad;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int Hk = p.num_kv_heads, G = p.group;
@@ -144,8 +144,10 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     }
     bad = __syncthreads_or(bad);
     if (bad || w.q_len == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      if (bad && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = kErrArgF4;
+      if (blockIdx.x == 0 && threadIdx.x == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (bad) p.hdr->error = kErrArgF4;
+      }
       return;
     }
     const int units = (w.kv_len + p.shape.unit - 1) / p.shape.unit;
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
     fence_mbarrier_init();
   }
-  if (threadIdx.x == 0) s_abort = 0;
+  if (threadIdx.x == 0) s_abort = s_bad = 0;
   __syncthreads();
   // A step's tiles come in runs that share a page; lane 2 r copies run r of K, lane
   // 2 r + 1 of V.  Its page number is read a step ahead.
@@ -555,12 +557,10 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   }
 
   // Join the warps' states (their rings are done with) and write the rows.
-  const int fault = __syncthreads_or((bad_page ? kErrArgF4 : 0)) ? kErrArgF4 : 0;
-  const bool gone = __syncthreads_or(failed);
-  // (The kernel before this one clears the error word.)
-  if (kStatic) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x == 0) {
-    const int error = gone ? kErrTimeoutF4 : fault;
+  if (bad_page) s_bad = 1;
+  __syncthreads();
+  const int error = s_abort ? kErrTimeoutF4 : (s_bad ? kErrArgF4 : 0);
+  if (!kStatic && threadIdx.x == 0) {
     if (kPlan) p.cta_error[blockIdx.x] = error;
     else if (error) atomicCAS(&p.hdr->error, 0, error);
   }
@@ -674,6 +674,12 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
         if (v == 0 && x < end && row0 + r >= 0) put(-1, r, c, acc, top, den, fp.v_scale);
       }
       cluster_sync();  // the others have read this CTA's memory
+    }
+    // The kernel before this one clears the error word; one CTA waits for its end, so that
+    // what follows this kernel follows that one.
+    if (threadIdx.x == 0 && (error || blockIdx.x == 0)) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (error) atomicCAS(&p.hdr->error, 0, error);
     }
     return;
   }

@@ -495,17 +495,18 @@ def test_a_prompt_in_chunks_then_tokens(cp, H, Hk, D):
 def test_streams_graphs_and_two_workspaces(cp):
     """A captured decoding step -- append, attention, read back -- replayed with other
     lengths and tokens, beside calls on another stream with a workspace of their own."""
-    for new, H in (([1, 1, 1], 8), ([1, 2, 3], 20), ([40, 1, 1], 8)):
+    for new, H, most in (([1, 1, 1], 8, 700), ([1, 2, 3], 20, 700), ([40, 1, 1], 8, 700),
+                         ([1, 1, 1], 8, 30000), ([1, 2, 3], 20, 30000), ([1, 2, 12], 8, 30000)):
         x = Batch4(new, [700, 20, 333], H, 2, 128, 16, seed=15, spoil=False)
         q, kc, vc, t, cu, kv = x.on_gpu()
         k, v = normal(x.T, 2, 128, seed=1).cuda(), normal(x.T, 2, 128, seed=2).cuda()
         first = kv.clone()
-        bounds = dict(max_seqlen=max(new), max_kv_len=700)
+        bounds = dict(max_seqlen=max(new), max_kv_len=most)
         kc1, vc1 = kc.clone(), vc.clone()
         cp.paged_append_fp4(k, v, kc1, vc1, t, cu, first)
         ref = cp.paged_attn_fp4(q, kc1, vc1, t, cu, first, **bounds)
         back = cp.paged_gather_fp4(kc1, vc1, t, cu, first, total_tokens=x.T)
-        kvs = i32([3, 3, 3] if max(new) < 40 else [40, 3, 3])
+        kvs = i32([max(n, 3) for n in new])
         ins = torch.zeros_like(k), torch.zeros_like(v)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
