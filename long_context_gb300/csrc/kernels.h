@@ -291,7 +291,7 @@ struct PagedShape {
   int round;       // CTAs resident at once (at most ctas)
   bool join;       // the last CTA of a split item joins it (else a merge kernel)
   bool plan;       // no schedule kernel: every warp works the list out (paged_plan.cuh)
-  bool fit;        // its splits as small as one round's slots allow
+  bool fit;        // splits are made to fill whole rounds of CTAs
 };
 
 struct PagedParams {
@@ -325,7 +325,10 @@ __device__ __forceinline__ int paged_rows_target(const PagedShape& s, long long 
                                                  int heads) {
   const long long lanes = static_cast<long long>(items) * heads;
   const bool one = 2 * lanes <= s.round;
-  const long long share = one ? s.round - lanes : s.ctas;
+  // (Every item has a last split that is half a share on average.)
+  const long long share = one     ? s.round - lanes
+                          : s.fit ? max(s.ctas - lanes / 2, s.ctas / 4ll)
+                                  : s.ctas;
   const long long target = (all * heads + share - 1) / share;
   const long long least = one ? 1 : s.min_units;
   return static_cast<int>(target < least ? least : (target > (1 << 30) ? (1 << 30) : target));
