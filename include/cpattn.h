@@ -624,13 +624,13 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  *                 aligned; one made for a batch does for smaller ones (total_q,
  *                 num_seqs, max_seqlen, max_kv_len) of the same heads.  With more than
  *                 64 rows of a KV head (max_seqlen * H / num_kv_heads) it holds the
- *                 batch's caches in bf16 (num_seqs * max_kv_len * num_kv_heads * 4 D
+ *                 batch's caches in 16 bits (num_seqs * max_kv_len * num_kv_heads * 4 D
  *                 bytes), which the call reads them into first.
  *   softmax_scale * k_scale has to be a normal float.
  * num_seqs * (max_kv_len / 128 + 1) < 2^31.
- * Precision: fp32 scores, softmax and sums over exact keys and values.  Up to 64 rows
- * of a KV head the queries are fp16 times a power of two per row (exact down to 2^-28
- * of the row's largest) and P is rounded to fp16; with more rows as cpattn_paged_attn.
+ * Precision: fp32 scores, softmax and sums over exact keys and values.  P is
+ * rounded to fp16 (2^-11 of each weight).  Up to 64 rows of a KV head the queries are
+ * fp16 times a power of two per row (exact down to 2^-28 of the row's largest).
  * One rounding of O to bf16.  Sums are taken in a fixed order: equal inputs under
  * equal bounds give equal bits.
  * All three enqueue on `stream`, read all lengths on the device, and return argument

@@ -18,6 +18,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace cpattn {
 
 constexpr int kFp4Tile = 16;        // tokens of a tile
@@ -60,12 +62,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t s) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

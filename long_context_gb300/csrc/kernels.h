@@ -302,6 +302,8 @@ struct PagedParams {
   int max_seqlen, max_kv_len;
   long long total_q, page_stride;
   float scale_log2;
+  bool v_half;   // tiles: v_cache holds fp16, to be multiplied by v_unit
+  float v_unit;
   __nv_bfloat16* out;
   float* lse;  // [total_q, num_heads] or null
   WsHeader* hdr;
@@ -362,12 +364,14 @@ constexpr int kFp4OutPage = 128;  // tokens of a bf16 page that the tile kernel 
 
 struct Fp4PagesParams {
   const uint8_t *k_cache, *v_cache;
-  __nv_bfloat16 *k_out, *v_out;      // [num_seqs * out_pages, 128, KV heads, D]
+  // [num_seqs * out_pages, 128, KV heads, D], without the caches' powers of two: keys in
+  // bf16, values in fp16 (both exactly).
+  __nv_bfloat16* k_out;
+  uint16_t* v_out;
   int* out_table;                    // [num_seqs, out_pages]
   const int *kv_lens, *page_table;
   int num_seqs, num_pages, page_shift, max_pages, kv_heads, out_pages, max_kv_len;
   long long page_stride;
-  float v_scale;
   WsHeader* hdr;
 };
 

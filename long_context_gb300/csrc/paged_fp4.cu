@@ -1,5 +1,5 @@
 // A paged KV cache in 4 bits (fp4.cuh): quantising new tokens into it, reading
-// tokens back, and reading a batch's caches into bf16 pages for the tile kernel.
+// tokens back, and reading a batch's caches into 16-bit pages for the tile kernel.
 //
 // Quantising, for 16 features x of a token and head (u the cache's power of two):
 //   s = e4m3(min(max(max|x| / (6 u), 2^-9), 448)),  c = e2m1(x / (s u)),
@@ -222,11 +222,11 @@ __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CachePa
   }
 }
 
-// Caches [0, kv_len) of every sequence to bf16 pages of 128 tokens, page i of
+// Caches [0, kv_len) of every sequence to 16-bit pages of 128 tokens, page i of
 // sequence b at b * out_pages + i, with the table that says so.  A CTA has a KV head and
 // every gridDim.x-th of the pages that there are (the bounds may be far above the
-// lengths), a warp a tile of it.  Keys are left without the cache's power of two (it is
-// in the softmax scale), values get it, exactly.
+// lengths), a warp a tile of it.  Keys in bf16, values in fp16, both exactly and without
+// the caches' powers of two: the softmax scale has the keys', the join of O the values'.
 template <int D>
 __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesParams p) {
   constexpr int LG = D / 8;
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesPar
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint8_t* tile = (w ? p.v_cache : p.k_cache) + at;
-        __nv_bfloat16* out = (w ? p.v_out : p.k_out) +
-                             ((to * kFp4OutPage + warp * kFp4Tile) * p.kv_heads + h) * D + c * 8;
+        uint16_t* out = (w ? p.v_out : reinterpret_cast<uint16_t*>(p.k_out)) +
+                        ((to * kFp4OutPage + warp * kFp4Tile) * p.kv_heads + h) * D + c * 8;
         uint32_t code[kFp4Tile / kRows], scale[kFp4Tile / kRows];
 #pragma unroll
         for (int i = 0; i < kFp4Tile / kRows; ++i) {
@@ -275,10 +275,19 @@ __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesPar
 #pragma unroll
         for (int i = 0; i < kFp4Tile / kRows; ++i) {
           const int r = i * kRows + lane / LG;
-          const float s = e4m3_value(scale[i]) * (w ? p.v_scale : 1.f);
+          uint4 v;
+          if (w) {
+            const uint32_t s = __byte_perm(e4m3x2_to_f16(scale[i]), 0, 0x1010);
+            uint32_t x[4];
+            fp4x8_to_f16(code[i], x);
+            v = make_uint4(mul_f16x2(x[0], s), mul_f16x2(x[1], s), mul_f16x2(x[2], s),
+                           mul_f16x2(x[3], s));
+          } else {
+            v = values8(code[i], e4m3_value(scale[i]));
+          }
           if (r < n)
             *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * p.kv_heads * D) =
-                gone ? make_uint4(0u, 0u, 0u, 0u) : values8(code[i], s);
+                gone ? make_uint4(0u, 0u, 0u, 0u) : v;
         }
       }
     }

@@ -40,7 +40,11 @@
 // with the rounding's remainder as a second operand (paged_rows.cu does that for up
 // to 16 rows) O's error against 64 bits is 0.0017 instead of 0.0020-0.0024, for
 // 1,012 instead of 746 us (2,048 tokens over 32,768, 32 / 8 heads of 128) and 1,068
-// instead of 688 us (4,864 over 32,768, 16 / 4 heads of 64).
+// instead of 688 us (4,864 over 32,768, 16 / 4 heads of 64).  Values that are exact in
+// fp16, those of a 4-bit cache's pages, take P in fp16: 2^-11 instead of 2^-8 of each
+// weight for the same instructions (error 0.0017, the same times).  Its range is a
+// weight's below 2^-32 of the largest; the reference moves whenever a tile's sum would
+// pass 2^15.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -52,8 +56,13 @@ namespace {
 
 constexpr float kNegInfT = -__builtin_huge_valf();
 constexpr float kLn2T = 0.69314718055994530942f;
-constexpr float kMoveByT = 8.0f;          // powers of two (see paged_rows.cu)
-constexpr float kMaxTileSum = 65536.0f;   // bound of a tile's sum of p
+// How P is held: bf16, or fp16 (pages of a 4-bit cache, whose values are exact in it).
+template <bool HALF>
+struct TileP {
+  static constexpr float kMoveBy = HALF ? 0.0f : 8.0f;            // powers of two (see paged_rows.cu)
+  static constexpr float kMaxSum = HALF ? 32768.0f : 65536.0f;    // bound of a tile's sum of p
+  static constexpr float kLift = HALF ? 7.0f : 0.0f;  // powers of two of p at the reference
+};
 
 enum : int { kErrArgT = 1, kErrTimeoutT = 6 };
 
@@ -97,13 +106,14 @@ __device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
 
 }  // namespace
 
-template <int D>
+template <int D, bool HALF>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CUtensorMap tm_o, const PagedParams p) {
   using C = TileCfg<D>;
+  using P = TileP<HALF>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The heads of a split run together; a head's blocks walk its keys in step,
@@ -269,7 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Lane 0 issues every MMA and never touches an mbarrier in the loop
       // (both warps 9 and 10 run the same number of rendezvous).
       constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, true);
+      // (Bits 7 and 10 are bf16 instead of fp16.)
+      constexpr uint32_t idesc_o =
+          idesc_bf16_f32(kBM, D, true) & ~(HALF ? (1u << 7) | (1u << 10) : 0u);
       const uint32_t hi_kq = static_cast<uint32_t>(sdesc_sw128(0, 16, 1024) >> 32);
       const uint32_t hi_v = static_cast<uint32_t>(sdesc_sw128(0, 16384, 1024) >> 32);
       const uint32_t lo_q =
@@ -496,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c_log2;
             const float m_new = fmaxf(m_run, m_tile);
-            if (__any_sync(0xffffffffu, m_new > m_run + kMoveByT)) {
+            if (__any_sync(0xffffffffu, m_new > m_run + P::kMoveBy)) {
               const float alpha = (m_run == kNegInfT) ? 0.f : ex2_approx(m_run - m_new);
               if (C::kRing && x > 0) {
                 ok = __all_sync(0xffffffffu, wait_bounded(&o_done[t], (x - 1) & 1, abort_flag));
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float mref = (m_run == kNegInfT) ? 0.f : m_run;
           const float2 c2 = make_float2(c_log2, c_log2);
-          const float2 nm2 = make_float2(-mref, -mref);
+          const float2 nm2 = make_float2(P::kLift - mref, P::kLift - mref);
           acc0 = make_float2(0.f, 0.f);
           acc1 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -533,11 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float2(__uint_as_float(sr[2 * k2]), __uint_as_float(sr[2 * k2 + 1])), c2, nm2);
             const float2 pp = make_float2(ex2_approx(xs.x), ex2_approx(xs.y));
             if (k2 & 1) acc1 = __fadd2_rn(acc1, pp); else acc0 = __fadd2_rn(acc0, pp);
-            pk[k2] = pack_bf16x2(pp.x, pp.y);
+            pk[k2] = HALF ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
           }
           if (with_max) break;
           const float l_tile = (acc0.x + acc1.x) + (acc0.y + acc1.y);
-          if (!__any_sync(0xffffffffu, !(l_tile <= kMaxTileSum))) break;
+          if (!__any_sync(0xffffffffu, !(l_tile <= P::kMaxSum))) break;
           with_max = true;
         }
         l_run += (acc0.x + acc1.x) + (acc0.y + acc1.y);
@@ -566,8 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         // Epilogue: O / l and LSE = m + ln l; zeros where no key is visible.
         const bool none = l_run == 0.f;
-        const float inv_l = none ? 0.f : 1.f / l_run;
-        const float lse = none ? kNegInfT : (m_run + __log2f(l_run)) * kLn2T;
+        const float inv_l = none ? 0.f : (HALF ? p.v_unit : 1.f) / l_run;
+        const float lse =
+            none ? kNegInfT : ((HALF ? m_run - P::kLift : m_run) + __log2f(l_run)) * kLn2T;
         uint32_t orr[D];
         if (n > 0) {
 #pragma unroll
@@ -669,11 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool HALF>
 static cudaError_t launch_paged_tile_t(const CUtensorMap& tq, const CUtensorMap& tk,
                                        const CUtensorMap& tv, const CUtensorMap& to,
                                        const PagedParams& p, cudaStream_t stream) {
-  auto kern = paged_tile_kernel<D>;
+  auto kern = paged_tile_kernel<D, HALF>;
   // The register split inside the kernel assumes exactly kLaunchRegs per
   // thread at launch; with any other count the raise could wait forever.
   static const int regs = [&] {
@@ -700,8 +713,11 @@ static cudaError_t launch_paged_tile_t(const CUtensorMap& tq, const CUtensorMap&
 cudaError_t launch_paged_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& to, const PagedParams& p, int D,
                               cudaStream_t stream) {
-  return D == 64 ? launch_paged_tile_t<64>(tq, tk, tv, to, p, stream)
-                 : launch_paged_tile_t<128>(tq, tk, tv, to, p, stream);
+  if (p.v_half)
+    return D == 64 ? launch_paged_tile_t<64, true>(tq, tk, tv, to, p, stream)
+                   : launch_paged_tile_t<128, true>(tq, tk, tv, to, p, stream);
+  return D == 64 ? launch_paged_tile_t<64, false>(tq, tk, tv, to, p, stream)
+                 : launch_paged_tile_t<128, false>(tq, tk, tv, to, p, stream);
 }
 
 }  // namespace cpattn

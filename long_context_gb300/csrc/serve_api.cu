@@ -190,7 +190,7 @@ bool merges(const PagedParams& p) {
 // Few rows over the 4-bit cache: blocks of 8, 16 or 32 rows and, above 32, three of 16
 // (40 rows over 20 caches of 5,000 to 15,000 keys, 4 heads of 128: 115 us, in two blocks
 // of 32 rows 124) or two of 32 (64 rows of 64: 82 and 89); with more than kFp4RowsMost
-// rows of a KV head the caches are read into bf16 pages and go through the tile kernel
+// rows of a KV head the caches are read into 16-bit pages and go through the tile kernel
 // (72 rows, the same caches: 170 by blocks and 177; 125 rows over nine caches 181 and 118;
 // 64 rows of 64 82 and 107).  Splits of less than 24 units cost more in joins than they
 // even out, and of more than 1 / 1368 of all work leave the SMs uneven (a token each of 64
@@ -238,7 +238,7 @@ int fp4_parts(const PagedParams& p) {
   return keys <= (parts > 1 ? 1024 : 4096) && lanes * parts < kInt31 ? parts : 0;
 }
 
-// The bf16 pages that the tile kernel reads: their table, keys and values.
+// The 16-bit pages that the tile kernel reads: their table, keys and values.
 struct Fp4Pages {
   int64_t pages;  // of a sequence
   size_t k_off, v_off, total;
@@ -271,7 +271,7 @@ size_t fp4_workspace(int64_t total_q, int32_t B, int32_t H, int32_t Hk, int32_t 
   return most;
 }
 
-// Whether every bf16 page of the batch has a number.
+// Whether every such page of the batch has a number.
 bool fp4_pages_ok(int32_t B, int32_t max_kv_len) {
   return (static_cast<int64_t>(max_kv_len) / kFp4OutPage + 1) * B < kInt31;
 }
@@ -826,7 +826,7 @@ extern "C" int cpattn_paged_attn_fp4(
     g.v_cache = static_cast<const uint8_t*>(v_cache);
     g.out_table = reinterpret_cast<int*>(ws + lay.total);
     g.k_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.total + pages.k_off);
-    g.v_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.total + pages.v_off);
+    g.v_out = reinterpret_cast<uint16_t*>(ws + lay.total + pages.v_off);
     g.kv_lens = kv_lens;
     g.page_table = page_table;
     g.num_seqs = num_seqs;
@@ -837,11 +837,12 @@ extern "C" int cpattn_paged_attn_fp4(
     g.out_pages = static_cast<int>(pages.pages);
     g.max_kv_len = max_kv_len;
     g.page_stride = page_stride;
-    g.v_scale = v_scale;
     g.hdr = p.hdr;
     if (pages.pages > 0 && launch_fp4_pages(g, head_dim, dev.num_sms, s) != cudaSuccess) return CPATTN_ERR_CUDA;
     p.k_cache = g.k_out;
-    p.v_cache = g.v_out;
+    p.v_cache = reinterpret_cast<const __nv_bfloat16*>(g.v_out);  // (16 bits a feature, as they are)
+    p.v_half = true;
+    p.v_unit = v_scale;
     p.page_table = g.out_table;
     p.max_pages = g.out_pages;
     p.num_pages = num_seqs * g.out_pages;

@@ -9,11 +9,11 @@ sum |q_i k_i| of the row; exponential, maximum and the weights of splits add 2^-
 and terms of l and O are added along chains of at most N / 32 + 700 (a warp takes two
 products a tile of 16 keys and every fourth step, a split has four warps, a merge
 joins at most 608 splits), 2^-24 each.
-With e the sum of these, numerator and denominator are both off by e.  Up to 64 rows
-of a KV head P is rounded to fp16 (2^-11 of each term, and below 2^-14, where the
-row's largest p is at least 2^11, by 2^-25: 2^-36 of the largest, N times); with more
-rows to bf16 (2^-8).  O is rounded to bf16 once (2^-8 |O|):
-|dO| <= 2^-8 |O| + (r + 2 e) size + N 2^-36 max |v|, and |dLSE| <= e + 2^-22 |LSE|."""
+With e the sum of these, numerator and denominator are both off by e.  P is rounded to
+fp16 (2^-11 of each term, and of one below 2^-14 by 2^-25).  Up to 64 rows of a KV head
+the row's largest p is at least 2^11, with more 2^7: f = 2^-36 or 2^-32 of it, N times.
+O is rounded to bf16 once (2^-8 |O|):
+|dO| <= 2^-8 |O| + (2^-11 + 2 e) size + N f max |v|, and |dLSE| <= e + 2^-22 |LSE|."""
 
 import numpy as np
 import pytest
@@ -100,9 +100,8 @@ class Batch4:
         N = max(self.kv)
         e = self.D * 2.0 ** -24 * span + 2.0 ** -18 + (N / 32 + 700) * 2.0 ** -24
         many = (bound or max(self.new)) * self.H // self.Hk > MANY
-        r = 2.0 ** -8 if many else 2.0 ** -11
-        tol = (2.0 ** -8 * np.abs(ref) + (r + 2 * e[..., None]) * size
-               + N * 2.0 ** -36 * np.abs(self.v).max())
+        tol = (2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * e[..., None]) * size
+               + N * 2.0 ** (-32 if many else -36) * np.abs(self.v).max())
         check(out[:n], ref, tol, "O")
         got = f64(lse[:n])
         assert np.array_equal(np.isneginf(got), np.isneginf(rl))
@@ -642,3 +641,21 @@ def test_two_calls_and_two_workspaces_at_once(cp):
         for i in range(2):
             assert cp.poll_error(ws[i]) == cp.OK
             xs[i].check(*outs[i])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rising_scores_of_many_rows(cp, D):
+    """The tile kernel's references move with every key tile, up and far up; and stay
+    where the scores fall."""
+    x = Batch4([40], [2000], 4, 1, D, 64, seed=23, spoil=False)
+    _, _, vc, t, cu, kv = x.on_gpu()
+    kc, junk = cp.alloc_fp4_cache(x.kc.shape[0], 64, 1, D), cp.alloc_fp4_cache(x.kc.shape[0], 64, 1, D)
+    for top in (2.0, -2.0, 30.0):
+        k = (torch.ones(2000, 1, D) * torch.linspace(-top, top, 2000).reshape(-1, 1, 1)).to(
+            torch.bfloat16).cuda()
+        cp.paged_append_fp4(k, k, kc, junk, t, i32([0, 2000]), kv)
+        x.k = o4.unpack(kc.cpu().numpy(), D)
+        x.q = torch.full((40, 4, D), 1.5, dtype=torch.bfloat16)
+        x.q[3] = -1.5
+        out, lse = cp.paged_attn_fp4(x.q.cuda(), kc, vc, t, cu, kv, **x.bounds())
+        x.check(out, lse)
