@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   using F = Fp4<D>;
   const PagedParams& p = fp.p;
   constexpr int kRows = C::kRows;
-  constexpr bool kMany = NT > 1;    // the queries in shared memory, permuted pairs of keys
+  constexpr bool kMany = NT > 1;    // the queries are in shared memory
   constexpr int kM = D / 16;        // products of a tile's scores
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kF4Warps][kRows], s_l[kF4Warps][kRows];
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   const int free_end = p.causal ? kv_len - q_len + max(row0, 0) / G + 1 : kv_len;
 
   // Lane (g, t) accumulates rows 2 t and 2 t + 1 of features g D / 8 + 2 i and + 1, i
-  // below D / 16: [i][feature][row] with permuted pairs, else [i / 2][feature][i % 2][row].
+  // below D / 16: [i][feature][row].
   float o[NT][D / 16][4];
   float m[NT][2];          // the references
   float2 off[NT], l[NT];   // 11 - m (11 without a reference) and the sums, by rows

@@ -838,9 +838,10 @@ extern "C" int cpattn_paged_attn_fp4(
     g.max_kv_len = max_kv_len;
     g.page_stride = page_stride;
     g.hdr = p.hdr;
-    if (pages.pages > 0 && launch_fp4_pages(g, head_dim, dev.num_sms, s) != cudaSuccess) return CPATTN_ERR_CUDA;
+    if (pages.pages > 0 && launch_fp4_pages(g, head_dim, dev.num_sms, s) != cudaSuccess)
+      return CPATTN_ERR_CUDA;
     p.k_cache = g.k_out;
-    p.v_cache = reinterpret_cast<const __nv_bfloat16*>(g.v_out);  // (16 bits a feature, as they are)
+    p.v_cache = reinterpret_cast<const __nv_bfloat16*>(g.v_out);  // (copied as they are)
     p.v_half = true;
     p.v_unit = v_scale;
     p.page_table = g.out_table;
