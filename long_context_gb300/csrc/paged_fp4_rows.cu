@@ -205,7 +205,10 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   // A step's tiles come in runs that share a page; lane 2 r copies run r of K, lane
   // 2 r + 1 of V.  Its page number is read a step ahead.
   const int page_tiles = 1 << (p.page_shift - 4);
-  const int run_tiles = min(span / kFp4Tile, page_tiles);
+  // (Aligned as the split's first key is, so that no run crosses a page's end: a step may
+  // have 128 keys, and a split starts at a multiple of 64.)
+  const int aligned = kv_lo > 0 ? max((kv_lo & -kv_lo) / kFp4Tile, 1) : page_tiles;
+  const int run_tiles = min(min(span / kFp4Tile, page_tiles), aligned);
   const int run_at = (lane >> 1) * run_tiles;
   const int copy_end = run_at * kFp4Tile < span ? kv_hi : 0;
   const int* pages = p.page_table + static_cast<size_t>(seq) * p.max_pages;

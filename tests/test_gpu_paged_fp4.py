@@ -659,3 +659,22 @@ def test_rising_scores_of_many_rows(cp, D):
         x.q[3] = -1.5
         out, lse = cp.paged_attn_fp4(x.q.cuda(), kc, vc, t, cu, kv, **x.bounds())
         x.check(out, lse)
+
+
+@pytest.mark.parametrize("size", [64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_splits_that_start_inside_a_page(cp, D, size):
+    """Splits begin at multiples of 64 keys, steps have up to 128, pages up to 256: by
+    the plan, by the list and in the parts of a cluster, for 8, 16 and 32 rows."""
+    for new, kv, H, Hk, bound in (([1, 2], [5000, 3333], 4, 4, 60000), ([1], [16000], 2, 2, 60000),
+                                  ([1] * 40, [1700 + 64 * b for b in range(40)], 8, 8, 60000),
+                                  ([1, 1, 1], [961, 700, 1023], 4, 4, 1023),
+                                  ([1], [450], 2, 1, 500), ([3], [900], 4, 1, 1000),
+                                  ([5, 3], [2900, 4000], 10, 2, 60000),
+                                  ([20], [3000], 3, 1, 60000)):
+        x = Batch4(new, kv, H, Hk, D, size, seed=51)
+        ws = cp.alloc_paged_fp4_workspace(x.T, len(kv), H, Hk, D, max(new), bound)
+        out, lse = cp.paged_attn_fp4(*x.on_gpu(), max_seqlen=max(new), max_kv_len=bound,
+                                     workspace=ws)
+        assert cp.poll_error(ws) == cp.OK
+        x.check(out, lse)
