@@ -628,6 +628,7 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  *                 bytes), which the call reads them into first.
  *   softmax_scale * k_scale has to be a normal float.
  * num_seqs * (max_kv_len / 128 + 1) < 2^31.
+ * The cache of a sequence without new tokens is not read.
  * Precision: fp32 scores, softmax and sums over exact keys and values.  P is
  * rounded to fp16 (2^-11 of each weight).  Up to 64 rows of a KV head the queries are
  * fp16 times a power of two per row (exact down to 2^-28 of the row's largest).

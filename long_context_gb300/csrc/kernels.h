@@ -369,7 +369,7 @@ struct Fp4PagesParams {
   __nv_bfloat16* k_out;
   uint16_t* v_out;
   int* out_table;                    // [num_seqs, out_pages]
-  const int *kv_lens, *page_table;
+  const int *cu_seqlens, *kv_lens, *page_table;
   int num_seqs, num_pages, page_shift, max_pages, kv_heads, out_pages, max_kv_len;
   long long page_stride;
   WsHeader* hdr;

@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(kF4Threads) fp4_gather_kernel(const Fp4CachePa
   }
 }
 
-// Caches [0, kv_len) of every sequence to 16-bit pages of 128 tokens, page i of
-// sequence b at b * out_pages + i, with the table that says so.  A CTA has a KV head and
-// every gridDim.x-th of the pages that there are (the bounds may be far above the
+// Caches [0, kv_len) of every sequence with new tokens to 16-bit pages of 128 tokens, page
+// i of sequence b at b * out_pages + i, with the table that says so.  A CTA has a KV head
+// and every gridDim.x-th of the pages that there are (the bounds may be far above the
 // lengths), a warp a tile of it.  Keys in bf16, values in fp16, both exactly and without
 // the caches' powers of two: the softmax scale has the keys', the join of O the values'.
 template <int D>
@@ -239,12 +239,17 @@ __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesPar
   const long long block = (1ll << p.page_shift) / kFp4Tile * Fp4<D>::kTileBytes;
   bool bad = false;
   int first = static_cast<int>(blockIdx.x);  // of this CTA's pages of sequence b
-  int kv_next = p.num_seqs > 0 ? __ldg(p.kv_lens) : 0;
+  int kv_next = __ldg(p.kv_lens), lo_next = __ldg(p.cu_seqlens), hi_next = __ldg(p.cu_seqlens + 1);
   for (int b = 0; b < p.num_seqs; ++b) {
-    const int kv = kv_next;
-    if (b + 1 < p.num_seqs) kv_next = __ldg(p.kv_lens + b + 1);
-    // (The schedule kernel reports lengths that are not valid.)
-    const bool valid = kv >= 0 && kv <= p.max_kv_len && kv <= cap;
+    const int kv = kv_next, lo = lo_next, hi = hi_next;
+    if (b + 1 < p.num_seqs) {
+      kv_next = __ldg(p.kv_lens + b + 1);
+      lo_next = hi;
+      hi_next = __ldg(p.cu_seqlens + b + 2);
+    }
+    // A sequence without new tokens is not read.  (The schedule kernel reports lengths
+    // that are not valid.)
+    const bool valid = hi > lo && kv >= 0 && kv <= p.max_kv_len && kv <= cap;
     const int n_pages = valid ? (kv + kFp4OutPage - 1) / kFp4OutPage : 0;
     const int* pages = p.page_table + static_cast<size_t>(b) * p.max_pages;
     int pg = first;

@@ -827,6 +827,7 @@ extern "C" int cpattn_paged_attn_fp4(
     g.out_table = reinterpret_cast<int*>(ws + lay.total);
     g.k_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.total + pages.k_off);
     g.v_out = reinterpret_cast<uint16_t*>(ws + lay.total + pages.v_off);
+    g.cu_seqlens = cu_seqlens;
     g.kv_lens = kv_lens;
     g.page_table = page_table;
     g.num_seqs = num_seqs;

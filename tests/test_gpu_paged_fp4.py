@@ -678,3 +678,16 @@ def test_splits_that_start_inside_a_page(cp, D, size):
                                      workspace=ws)
         assert cp.poll_error(ws) == cp.OK
         x.check(out, lse)
+
+
+@pytest.mark.parametrize("bound,most", [(1, 700), (1, 30000), (12, 30000), (100, 700)])
+def test_sequences_without_new_tokens_are_not_read(cp, bound, most):
+    """Their page table may hold anything: a server's sequences that pause a step."""
+    x = Batch4([1, 0, 1, 0], [200, 700, 65, 300], 8, 2, 64, 32, seed=61)
+    q, kc, vc, t, cu, kv = x.on_gpu()
+    t[1], t[3] = 2 ** 30, -5
+    ws = cp.alloc_paged_fp4_workspace(x.T, 4, 8, 2, 64, bound, most)
+    out, lse = cp.paged_attn_fp4(q, kc, vc, t, cu, kv, max_seqlen=bound, max_kv_len=most,
+                                 workspace=ws)
+    assert cp.poll_error(ws) == cp.OK
+    x.check(out, lse, bound=bound)
