@@ -626,7 +626,7 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  *                 64 rows of a KV head (max_seqlen * H / num_kv_heads) it holds the
  *                 batch's caches in 16 bits (num_seqs * max_kv_len * num_kv_heads * 4 D
  *                 bytes), which the call reads them into first.
- *   softmax_scale * k_scale has to be a normal float.
+ *   softmax_scale * k_scale has to be a normal float, and that times log2(e).
  * num_seqs * (max_kv_len / 128 + 1) < 2^31.
  * The cache of a sequence without new tokens is not read.
  * Precision: fp32 scores, softmax and sums over exact keys and values.  P is

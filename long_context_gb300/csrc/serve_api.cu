@@ -768,8 +768,11 @@ extern "C" int cpattn_paged_attn_fp4(
   if (group > kPagedMaxGroup || !fp4_pages_ok(num_seqs, max_kv_len)) return CPATTN_ERR_UNSUPPORTED;
   if (!(std::isfinite(softmax_scale) && softmax_scale > 0.f) || (causal != 0 && causal != 1))
     return CPATTN_ERR_INVALID_ARG;
-  const float scale_log2 = softmax_scale * 1.4426950408889634f * k_scale;
-  if (!std::isnormal(scale_log2)) return CPATTN_ERR_INVALID_ARG;
+  // (The power of two first: a softmax scale that is no normal float, or one near the largest,
+  // keeps its bits only so.)
+  const float scale = softmax_scale * k_scale;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isnormal(scale) || !std::isnormal(scale_log2)) return CPATTN_ERR_INVALID_ARG;
   const bool any = total_q > 0 && num_seqs > 0;
   if (any) {
     if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16) || out == q ||
