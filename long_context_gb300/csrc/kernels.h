@@ -273,6 +273,12 @@ struct alignas(16) PagedMerge {
   int n, pad[3];
 };
 
+// What a kernel of the paged attention puts into the error word (statuses of cpattn.h).
+// The merge after a plan takes the words of all CTAs together, bit by bit.
+constexpr int kPagedBad = 1;   // CPATTN_ERR_INVALID_ARG
+constexpr int kPagedLate = 6;  // CPATTN_ERR_DEVICE_TIMEOUT
+static_assert((kPagedBad & kPagedLate) == 0, "told apart in the words of all CTAs");
+
 struct PagedLayout {
   size_t first_off, work_off, merge_off, arrived_off, error_off, o_off, lse_off, total;
   int64_t max_work;   // splits of one KV head
@@ -311,7 +317,7 @@ struct PagedParams {
   PagedWork* work;    // [max_work]
   PagedMerge* merge;  // [max_slots / 2]
   int* arrived;       // [max_slots / 2, num_kv_heads]: splits that are done (join)
-  int* cta_error;     // [max_work, num_kv_heads]: bad pages seen (plan)
+  int* cta_error;     // [max_work, num_kv_heads]: 0, kPagedBad or kPagedLate (plan)
   float* o_part;      // [max_slots, num_kv_heads, rows, D], normalised
   float* lse_part;    // [max_slots, num_kv_heads, rows], natural log
   long long max_work, max_slots;
@@ -360,7 +366,7 @@ struct Fp4CacheParams {
 cudaError_t launch_fp4_append(const Fp4CacheParams& p, int D, cudaStream_t stream);
 cudaError_t launch_fp4_gather(const Fp4CacheParams& p, int D, cudaStream_t stream);
 
-constexpr int kFp4OutPage = 128;  // tokens of a bf16 page that the tile kernel reads
+constexpr int kFp4OutPage = 128;  // tokens of a 16-bit page that the tile kernel reads
 
 struct Fp4PagesParams {
   const uint8_t *k_cache, *v_cache;

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kF4Threads) fp4_pages_kernel(const Fp4PagesPar
   }
   // The schedule before this clears the error word.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (bad && lane == 0) atomicCAS(&p.hdr->error, 0, kErrArgF);
+  if (bad && lane == 0) atomicCAS(&p.hdr->error, 0, kPagedBad);
 }
 
 static dim3 fp4_grid(const Fp4CacheParams& p, int lanes, int run) {

@@ -65,8 +65,6 @@ constexpr float kMaxSumF = 32768.f;  // of a lane's weights of a row in one pass
 
 constexpr int kF4MaxParts = 8;       // CTAs of a portable cluster
 
-enum : int { kErrArgF4 = 1, kErrTimeoutF4 = 6 };
-
 // Where a CTA's work comes from.
 enum class Fp4Work {
   kList,   // the schedule kernel's list
@@ -146,7 +144,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
     if (bad || w.q_len == 0) {
       if (blockIdx.x == 0 && threadIdx.x == 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (bad) p.hdr->error = kErrArgF4;
+        if (bad) p.hdr->error = kPagedBad;
       }
       return;
     }
@@ -562,7 +560,7 @@ __global__ void __launch_bounds__(kF4RowsThreads, Fp4RowsCfg<D, NT>::kCtas)
   // Join the warps' states (their rings are done with) and write the rows.
   if (bad_page) s_bad = 1;
   __syncthreads();
-  const int error = s_abort ? kErrTimeoutF4 : (s_bad ? kErrArgF4 : 0);
+  const int error = s_abort ? kPagedLate : (s_bad ? kPagedBad : 0);
   if (!kStatic && threadIdx.x == 0) {
     if (kPlan) p.cta_error[blockIdx.x] = error;
     else if (error) atomicCAS(&p.hdr->error, 0, error);

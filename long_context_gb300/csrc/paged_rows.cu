@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kPrThreads, 2) paged_rows_kernel(const PagedPa
   cp_async_wait<0>();
   const bool any_bad = __syncthreads_or(bad_page);
   if (threadIdx.x == 0) {
-    if (PLAN) p.cta_error[blockIdx.x] = any_bad ? 1 : 0;
-    else if (any_bad) atomicCAS(&p.hdr->error, 0, 1);  // CPATTN_ERR_INVALID_ARG
+    if (PLAN) p.cta_error[blockIdx.x] = any_bad ? kPagedBad : 0;
+    else if (any_bad) atomicCAS(&p.hdr->error, 0, kPagedBad);
   }
   float* so = reinterpret_cast<float*>(smem) + warp * kRows * D;
 #pragma unroll

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(128) paged_schedule_few_kernel(const PagedPara
                                   kv < 0 || kv > p.max_kv_len || kv > cap ||
                                   (lane == 0 && lo != 0))) {
     if (threadIdx.x == 0) {
-      p.hdr->error = 1;  // CPATTN_ERR_INVALID_ARG
+      p.hdr->error = kPagedBad;
       p.hdr->n_items = 0;
       p.hdr->pad[0] = 0;
     }
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(NT) paged_schedule_kernel(const PagedParams p)
   __syncthreads();
   if (s_bad) {
     if (tid == 0) {
-      p.hdr->error = 1;  // CPATTN_ERR_INVALID_ARG
+      p.hdr->error = kPagedBad;
       p.hdr->n_items = 0;
       p.hdr->pad[0] = 0;
     }
@@ -534,11 +534,10 @@ __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(const PagedPara
     int error = 0;
     for (int i = threadIdx.x; i < plan.splits * p.num_kv_heads; i += kPmThreads)
       error |= __ldcg(p.cta_error + i);
-    const bool bad = __syncthreads_or(plan.bad || (error & 1));
-    const bool late = __syncthreads_or(error & 6);
+    const bool bad = __syncthreads_or(plan.bad || (error & kPagedBad));
+    const bool late = __syncthreads_or(error & kPagedLate);
     if (threadIdx.x == 0) {
-      // CPATTN_ERR_INVALID_ARG, CPATTN_ERR_DEVICE_TIMEOUT
-      p.hdr->error = bad ? 1 : (late ? 6 : 0);
+      p.hdr->error = bad ? kPagedBad : (late ? kPagedLate : 0);
       p.hdr->n_items = plan.splits;
       p.hdr->pad[0] = plan.merges;
     }

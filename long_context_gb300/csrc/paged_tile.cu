@@ -64,8 +64,6 @@ struct TileP {
   static constexpr float kLift = HALF ? 7.0f : 0.0f;  // powers of two of p at the reference
 };
 
-enum : int { kErrArgT = 1, kErrTimeoutT = 6 };
-
 template <int D>
 struct TileCfg {
   static constexpr int kHalves = D / 64;          // 128-byte swizzle atoms
@@ -173,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (my_key >= kBN || key >= kv_len) return -1;
     const int page = __ldg(pages + (key >> p.page_shift));
     if (page >= 0 && page < p.num_pages) return page;
-    atomicCAS(&p.hdr->error, 0, kErrArgT);
+    atomicCAS(&p.hdr->error, 0, kPagedBad);
     return p.num_pages;  // out of range: the copy fills zeros
   };
   auto copy_tile = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int kv0, int page,
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) {
         if (!ok) {
-          atomicCAS(&p.hdr->error, 0, kErrTimeoutT);
+          atomicCAS(&p.hdr->error, 0, kPagedLate);
           *abort_flag = 1;
         }
         // Drain: every copy issued into shared memory must land before exit.
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (lane == 0 && !ok) {
-        atomicCAS(&p.hdr->error, 0, kErrTimeoutT);
+        atomicCAS(&p.hdr->error, 0, kPagedLate);
         *abort_flag = 1;
       }
       __syncwarp();
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
       }
       if (!ok) {
-        atomicCAS(&p.hdr->error, 0, kErrTimeoutT);
+        atomicCAS(&p.hdr->error, 0, kPagedLate);
         *abort_flag = 1;
       }
     }

@@ -17,6 +17,8 @@ namespace {
 
 constexpr size_t kServeAlign = 256;
 constexpr int64_t kInt31 = int64_t(1) << 31;
+static_assert(kPagedBad == CPATTN_ERR_INVALID_ARG && kPagedLate == CPATTN_ERR_DEVICE_TIMEOUT,
+              "the kernels' words are the header's");
 
 inline size_t serve_align(size_t x) { return (x + kServeAlign - 1) / kServeAlign * kServeAlign; }
 
