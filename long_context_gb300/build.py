@@ -92,8 +92,9 @@ def _build_variant(name, define, force):
 def build_fault_injection(force=False):
     """Test-only variant ``libcpattn_fault.so`` built with
     ``-DCPATTN_FAULT_INJECT_DROP_P``: the first CTA of the attention kernels
-    (forward, backward, paged tiles) skips one hand-off so that a bounded device
-    wait runs out.  Used by the failure detection tests; never loaded by the
+    (forward, backward, paged tiles) skips one hand-off, or does not start a copy that
+    it waits for (few rows over the 4-bit cache), so that a bounded device wait runs
+    out.  Used by the failure detection tests; never loaded by the
     package."""
     return _build_variant("cpattn_fault", "CPATTN_FAULT_INJECT_DROP_P", force)
 
