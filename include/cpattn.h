@@ -614,7 +614,9 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  * - cu_seqlens[b] of each sequence's kv_lens[b] (all of them, where that is
  * kv_lens[b]): k_out, v_out bf16 [T, num_kv_heads, D] with token strides as
  * cpattn_paged_append's inputs, exactly the cached values.  Packed keys and values
- * as cpattn_fwd, cpattn_decode and cpattn_paged_append take them.
+ * as cpattn_paged_append takes them, and, of a cache with a KV head for every query
+ * head, as cpattn_fwd and cpattn_decode do (with grouped heads those two want each KV
+ * head repeated).
  *   status        as there; rows of a token without a place, and the rows behind the
  *                 last sequence, are left as they were.
  *
