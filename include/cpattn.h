@@ -631,8 +631,11 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  *   softmax_scale * k_scale has to be a normal float, and that times log2(e).
  * num_seqs * (max_kv_len / 128 + 1) < 2^31.
  * The cache of a sequence without new tokens is not read.
- * Precision: fp32 scores, softmax and sums over exact keys and values.  P is
- * rounded to fp16 (2^-11 of each weight).  Up to 64 rows of a KV head the queries are
+ * Precision: fp32 scores, softmax and sums over exact keys and values.  For its
+ * product with V, P is rounded to fp16: a weight is off by at most 2^-11 of itself or, if
+ * that is more, by 2^-36 of the row's largest weight (2^-32 with more than 64 rows of a
+ * KV head), and is zero where it is smaller than that; the sum that O is divided by
+ * has every weight unrounded.  Up to 64 rows of a KV head the queries are
  * fp16 times a power of two per row (exact down to 2^-28 of the row's largest).
  * One rounding of O to bf16.  Sums are taken in a fixed order: equal inputs under
  * equal bounds give equal bits.

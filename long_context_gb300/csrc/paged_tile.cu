@@ -42,9 +42,10 @@
 // 1,012 instead of 746 us (2,048 tokens over 32,768, 32 / 8 heads of 128) and 1,068
 // instead of 688 us (4,864 over 32,768, 16 / 4 heads of 64).  Values that are exact in
 // fp16, those of a 4-bit cache's pages, take P in fp16: 2^-11 instead of 2^-8 of each
-// weight for the same instructions (error 0.0017, the same times).  Its range is a
-// weight's below 2^-32 of the largest; the reference moves whenever a tile's sum would
-// pass 2^15.
+// weight for the same instructions (error 0.0017, the same times).  p is 2^7 at the
+// reference: fp16 keeps its 11 bits of weights down to 2^-21 of that, is off by at most
+// 2^-32 of it below and has zero for weights smaller than that, which l still sums; the
+// reference moves whenever a tile's sum would pass 2^15.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
