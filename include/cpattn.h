@@ -608,7 +608,8 @@ int cpattn_paged_attn(const void* q, const void* k_cache, const void* v_cache,
  * The bytes are those of exact arithmetic.  A group with a NaN or an infinity gets
  * s = NaN and reads back as NaNs.  A zero has no sign.
  *   k, v, status, and what becomes of a token without a place or of two with one
- *   place: as cpattn_paged_append.
+ *   place: as cpattn_paged_append (parts of either: the codes of one and the scale of
+ *   the other among them, which are neither's value).
  *
  * cpattn_paged_gather_fp4 -- reads the same tokens back, the last cu_seqlens[b + 1]
  * - cu_seqlens[b] of each sequence's kv_lens[b] (all of them, where that is
