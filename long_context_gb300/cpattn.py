@@ -919,7 +919,9 @@ def paged_attn_fp4(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, max_
     ``(out, lse)``.
 
     ``k_cache, v_cache``: see :func:`alloc_fp4_cache`; ``k_scale``, ``v_scale``: as
-    given to :func:`paged_append_fp4`; the others as :func:`paged_attn`'s.
+    given to :func:`paged_append_fp4`; the others as :func:`paged_attn`'s.  With
+    ``max_seqlen * H / Hk`` above 64 all caches of the batch are read into the workspace
+    in 16 bits first: give a prompt's chunk and decoding sequences a call each.
     """
     return _binding().paged_attn_fp4(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens,
                                      max_seqlen, max_kv_len, k_scale, v_scale, softmax_scale,
