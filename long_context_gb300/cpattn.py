@@ -905,7 +905,8 @@ def paged_fp4_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_di
 def alloc_paged_fp4_workspace(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
                               max_kv_len, device=None):
     """A device workspace sized for :func:`paged_attn_fp4` (torch-owned), for this batch
-    and smaller ones of the same heads."""
+    and smaller ones of the same heads.  With ``max_seqlen * num_heads / num_kv_heads`` above
+    64 it has room for ``num_seqs * max_kv_len`` keys and values in 16 bits."""
     n = paged_fp4_workspace_size(total_q, num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen,
                                  max_kv_len)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
